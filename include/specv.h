@@ -445,6 +445,131 @@ specv_status specv_verify_noalloc(const void *target_logits, const void *draft_l
                                   int32_t K, int32_t V, specv_dtype dtype, specv_mode mode,
                                   int32_t *out_tokens, int32_t *out_n_accepted, void *stream);
 
+/*
+ * specv_token_logprobs -- log probabilities of given tokens under rows of
+ * logits, with each row's entropy and its most likely alternatives: what a
+ * serving interface returns beside the tokens that the verify step emitted, and
+ * what a training step scores.  (The pages have no counterpart.)
+ *
+ *   logits         element (b, n, v) at b * stride_b + n * stride_n + v
+ *                  (elements; strides >= 0, e.g. the target rows of specv_verify
+ *                  with N = K + 1, or rows of a padded vocabulary)
+ *   tokens         [B][N]  int32  specv_verify's out_tokens, or any tokens
+ *   B, N, V >= 1, B * N < 2^31
+ *   top_n          0..32 alternatives per row
+ *   out_logprob    [B][N]  fp32   ln p(token)
+ *   out_entropy    [B][N]  fp32   -sum_v p_v ln p_v
+ *   out_stats      [B][N][2] fp32 (max_v z_v, ln sum_v exp(z_v - max)): their sum is the
+ *                                 row's log-normaliser; kept for the gradient
+ *   out_top_tokens [B][N][top_n] int32, out_top_logprobs [B][N][top_n] fp32:
+ *                  the most likely entries in order, ties by the lower token
+ *                  (both NULL when top_n == 0)
+ *
+ * A token of -1 is no token: its row is not read; log probability, entropy and
+ * stats are 0, alternatives (-1, -inf).  Any other token outside [0, V) gives
+ * NaN and alternatives (-1, NaN).  A -inf logit masks its entry, which is no
+ * alternative: places without one hold (-1, -inf).  A row that masks every entry
+ * gives log probability -inf, entropy 0 and stats (-inf, 0).  A row that holds a
+ * NaN or +inf has no distribution: NaN, alternatives (-1, NaN).
+ * Sums are fp32.  No scratch, no allocation; asynchronous on `stream`; host
+ * argument errors return SPECV_ERR_INVALID_ARG and launch nothing.
+ */
+specv_status specv_token_logprobs(const void *logits, const int32_t *tokens, int64_t B, int32_t N,
+                                  int32_t V, int64_t stride_b, int64_t stride_n,
+                                  specv_dtype dtype, int32_t top_n, float *out_logprob,
+                                  float *out_entropy, float *out_stats, int32_t *out_top_tokens,
+                                  float *out_top_logprobs, void *stream);
+
+/*
+ * specv_token_logprobs_backward -- the gradient of a scalar with respect to the
+ * logits of specv_token_logprobs, from its gradients with respect to the log
+ * probabilities (g) and the entropies (h):
+ *   out_grad[b][n][v] = g (1[v = token] - p_v) - h p_v (ln p_v + entropy).
+ *
+ *   logits, tokens, B, N, V, stride_b, stride_n, dtype   as the forward call
+ *   stats [B][N][2], entropy [B][N]   what the forward call wrote
+ *   grad_logprob [B][N]   fp32
+ *   grad_entropy [B][N]   fp32, or NULL (zeros)
+ *   out_grad     [B][N][V]  dtype, contiguous; may be `logits` itself when that
+ *                           is contiguous (in place)
+ * Rows of token -1 and rows that mask every entry get zeros; rows with an
+ * invalid token or NaN stats get NaN.  Errors as the forward call.
+ */
+specv_status specv_token_logprobs_backward(const void *logits, const int32_t *tokens,
+                                           const float *stats, const float *entropy,
+                                           const float *grad_logprob, const float *grad_entropy,
+                                           int64_t B, int32_t N, int32_t V, int64_t stride_b,
+                                           int64_t stride_n, specv_dtype dtype, void *out_grad,
+                                           void *stream);
+
+typedef enum {
+    SPECV_FORWARD_KL = 0, /* KL(p_t || q): sum_v p_t,v (ln p_t,v - ln q_v) */
+    SPECV_REVERSE_KL = 1  /* KL(q || p_t): sum_v q_v (ln q_v - ln p_t,v) */
+} specv_divergence;
+
+/*
+ * specv_distill -- the loss that fits a draft to its target, with its gradient
+ * with respect to the draft logits: per drafted position the divergence between
+ * the target softmax p_t and the draft softmax q of the rows that the verify
+ * step has read.  (The pages raise the acceptance rate by training the drafter
+ * on the target; they give no formula.)
+ *
+ *   target_logits  row (b, i) at b * target_stride_b + i * target_stride_k, i < K
+ *                  (specv_verify's [B][K+1][V]: target_stride_b = (K + 1) V)
+ *   draft_logits   row (b, i) at b * draft_stride_b + i * draft_stride_k
+ *   weight         [B][K] fp32, or NULL (ones); a position of weight 0 is not
+ *                  read: loss 0, gradient 0
+ *   B, K, V >= 1, B * K < 2^31; strides in elements, >= 0
+ *   out_loss       [B][K] fp32   weight * divergence
+ *   out_grad       [B][K][V] dtype, contiguous: d(sum of out_loss) / d draft_logits,
+ *                  or NULL (the loss alone); may be draft_logits itself when that
+ *                  is contiguous (in place)
+ *
+ * An entry whose leading probability (p_t forward, q reverse) is zero in fp32
+ * adds nothing.  An entry of positive leading probability that the other row
+ * masks (-inf) makes the loss +inf; the forward gradient weight * (q - p_t) is
+ * still written, the reverse gradient is NaN at every entry of positive q.  A
+ * pair in which either row masks every entry has no divergence: loss 0, gradient
+ * 0.  A NaN or +inf logit gives NaN for its pair.  Sums are fp32; a loss below
+ * zero by rounding is written as 0.  No scratch, no allocation; asynchronous on
+ * `stream`; host argument errors return SPECV_ERR_INVALID_ARG, launching nothing.
+ */
+specv_status specv_distill(const void *target_logits, const void *draft_logits,
+                           const float *weight, int64_t B, int32_t K, int32_t V,
+                           int64_t target_stride_b, int64_t target_stride_k,
+                           int64_t draft_stride_b, int64_t draft_stride_k, specv_dtype dtype,
+                           specv_divergence kind, float *out_loss, void *out_grad, void *stream);
+
+/* One gradient of specv_clip_grads: `count` contiguous elements. */
+typedef struct {
+    const void *grad; /* device pointer, aligned to its element */
+    void *out;        /* where the clipped values go: `grad` itself, or memory that
+                       * overlaps no gradient */
+    int64_t count;    /* >= 0 */
+    int64_t dtype;    /* a specv_dtype */
+} specv_grad;
+
+/*
+ * specv_clip_grads -- the 2-norm over all elements of n gradients, and clipping
+ * to a largest norm:
+ *   norm = sqrt(sum x^2),  c = min(1, max_norm / (norm + 1e-6)),  out = c x
+ * (rounded once to the gradient's type).
+ *
+ *   grads     [n] on the HOST, read before the call returns; n >= 0
+ *   max_norm  >= 0; +inf only measures
+ *   out_norm  fp32, device: the norm before clipping
+ *
+ * With c = 1 a gradient clipped in place is not written.  A norm that is not
+ * finite leaves the values as they are (copied when out differs from grad), so
+ * that a training loop can look at the norm and drop the step.  Squares are
+ * summed in fp32 within 8192 elements and in fp64 beyond, in a fixed order; an
+ * element beyond 1.8e19 overflows its square and with it the norm.  No element
+ * may be listed twice.  Scratch: at most 64 KiB in the stream's workspace (see
+ * specv_verify).  Asynchronous on `stream`.
+ */
+specv_status specv_clip_grads(const specv_grad *grads, int64_t n, float max_norm, float *out_norm,
+                              void *stream);
+
 /* Human-readable name of a status. Never NULL. */
 const char *specv_status_string(specv_status status);
 

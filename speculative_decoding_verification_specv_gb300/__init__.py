@@ -25,7 +25,9 @@ from . import build as _build
 
 __all__ = ["SpecvError", "PROB_MIX", "LOGIT_MIX", "GREEDY", "F32", "BF16", "load", "lib_path",
            "verify", "verify_host", "verify_debug", "verify_tree", "acceptance_rates", "choose_k",
-           "AdaptiveK", "plan", "status_string", "EXPORTED_SYMBOLS"]
+           "AdaptiveK", "plan", "status_string", "EXPORTED_SYMBOLS", "token_logprobs",
+           "token_logprobs_backward", "TokenLogprobs", "distill", "FORWARD_KL", "REVERSE_KL",
+           "clip_grads"]
 
 PROB_MIX = 0
 LOGIT_MIX = 1
@@ -36,7 +38,8 @@ BF16 = 1
 EXPORTED_SYMBOLS = ("specv_verify", "specv_verify_debug", "specv_plan", "specv_status_string",
                     "specv_last_cuda_error", "specv_version", "specv_verify_noalloc",
                     "specv_acceptance_rates", "specv_choose_k", "specv_verify_tree",
-                    "specv_verify_host")
+                    "specv_verify_host", "specv_token_logprobs",
+                    "specv_token_logprobs_backward", "specv_distill", "specv_clip_grads")
 
 _STATUS = {0: "SPECV_OK", 1: "SPECV_ERR_INVALID_ARG", 2: "SPECV_ERR_UNSUPPORTED",
            3: "SPECV_ERR_CUDA", 4: "SPECV_ERR_NO_MEMORY"}
@@ -110,6 +113,17 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         lib.specv_shard_bounds.restype = ctypes.c_int
         lib.specv_verify_sharded_host.argtypes = common + [i32, vp]
         lib.specv_verify_sharded_host.restype = ctypes.c_int
+        lib.specv_token_logprobs.argtypes = [vp, vp, i64, i32, i32, i64, i64, ctypes.c_int, i32, vp,
+                                             vp, vp, vp, vp, vp]
+        lib.specv_token_logprobs.restype = ctypes.c_int
+        lib.specv_token_logprobs_backward.argtypes = [vp] * 6 + [i64, i32, i32, i64, i64,
+                                                                 ctypes.c_int, vp, vp]
+        lib.specv_token_logprobs_backward.restype = ctypes.c_int
+        lib.specv_distill.argtypes = [vp, vp, vp, i64, i32, i32, i64, i64, i64, i64, ctypes.c_int,
+                                      ctypes.c_int, vp, vp, vp]
+        lib.specv_distill.restype = ctypes.c_int
+        lib.specv_clip_grads.argtypes = [vp, i64, ctypes.c_float, vp, vp]
+        lib.specv_clip_grads.restype = ctypes.c_int
         dbl = ctypes.c_double
         lib.specv_choose_k.argtypes = [dbl, dbl, dbl, dbl, i32, i32]
         lib.specv_choose_k.restype = ctypes.c_int32
@@ -459,3 +473,7 @@ def plan(B: int, K: int, V: int, dtype: int = F32, mode: int = PROB_MIX) -> dict
 def raw_call(name: str, *args) -> int:
     """Call an entry point of the C ABI with raw arguments (tests of the boundary)."""
     return int(getattr(load(), name)(*args))
+
+
+from .scoring import (FORWARD_KL, REVERSE_KL, TokenLogprobs, clip_grads, distill,  # noqa: E402
+                      token_logprobs, token_logprobs_backward)

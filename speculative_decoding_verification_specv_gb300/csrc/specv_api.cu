@@ -1219,6 +1219,21 @@ struct NvtxRange {
 
 }  // namespace
 
+namespace specv {
+
+int device_ready(int *sms) { return ensure_device(sms, nullptr); }
+
+bool stream_scratch(cudaStream_t stream, size_t bytes, void **data) {
+  int dev = 0;
+  unsigned *count = nullptr;
+  return cudaGetDevice(&dev) == cudaSuccess &&
+         cached_workspace(dev, stream, 0, bytes, &count, data);
+}
+
+int cluster_override() { return cluster_from_env(); }
+
+}  // namespace specv
+
 extern "C" {
 
 specv_status specv_verify(const void *target_logits, const void *draft_logits,

@@ -10,6 +10,15 @@ namespace specv {
 // (per host thread).
 void note_cuda_error(cudaError_t e);
 
+// Host state of the C-ABI layer (specv_api.cu), for its second part
+// (specv_api_ops.cu).  device_ready: a specv_status as an int, with the current
+// device's SM count.  stream_scratch: the stream's cached scratch with room for
+// `bytes` bytes, or false (the caller then takes stream-ordered memory).
+// cluster_override: SPECV_CLUSTER_SIZE, 0 if unset.
+int device_ready(int *sms);
+bool stream_scratch(cudaStream_t stream, size_t bytes, void **data);
+int cluster_override();
+
 constexpr int kRowThreads = 256;   // threads per CTA of the cluster row kernel
 constexpr int kMaxCluster = 16;    // largest cluster (non-portable size, opt-in)
 constexpr int kTileThreads = 256;  // threads per CTA of the small-vocabulary kernel
@@ -255,5 +264,79 @@ cudaError_t tile_prepare(int max_smem_bytes);
 int tile_blocks_per_sm(int dtype_bf16, int mode, int smem_bytes);
 cudaError_t tile_launch(const TileArgs &a, int dtype_bf16, int mode, int64_t grid, int smem_bytes,
                         cudaStream_t stream);
+
+// ---------------------------------------------------------------------------
+// Operators on the step's logits: log probabilities, distillation, clipping.
+
+// Arguments of the log-probability kernel: rows (b, n) of a [B][N][V] view.
+struct LogprobArgs {
+  const void *logits;        // element (b, n, v) at b * stride_b + n * stride_n + v
+  const int32_t *tokens;     // [R]: -1 = no token, the row is not read
+  int64_t R;                 // B * N rows
+  int N;
+  int V;
+  int64_t stride_b, stride_n;
+  int top_n;                 // alternatives per row, 0..kMaxTop
+  float *logprob;            // [R]
+  float *entropy;            // [R]
+  float2 *stats;             // [R]: (max, ln sum exp(z - max))
+  int32_t *top_tokens;       // [R][top_n] (null when top_n == 0)
+  float *top_logprobs;       // [R][top_n]
+};
+constexpr int kMaxTop = 32;  // one alternative per lane of a warp
+cudaError_t logprobs_launch(const LogprobArgs &a, int dtype_bf16, cudaStream_t stream);
+
+// Arguments of the log-probability gradient kernel.
+struct LogprobGradArgs {
+  const void *logits;
+  const int32_t *tokens;     // [R]
+  const float2 *stats;       // [R]
+  const float *entropy;      // [R]
+  const float *grad_logprob; // [R]
+  const float *grad_entropy; // [R], or null: zeros
+  int64_t R;
+  int N;
+  int V;
+  int64_t stride_b, stride_n;
+  void *out;                 // [R][V] contiguous
+};
+cudaError_t logprobs_grad_launch(const LogprobGradArgs &a, int dtype_bf16, cudaStream_t stream);
+
+// Arguments of the distillation kernel: row pairs (b, i).
+struct DistillArgs {
+  const void *target;        // row (b, i) at b * target_stride_b + i * target_stride_k
+  const void *draft;         // row (b, i) at b * draft_stride_b + i * draft_stride_k
+  const float *weight;       // [B][K], or null: ones
+  int64_t B;
+  int K;
+  int V;
+  int64_t target_stride_b, target_stride_k, draft_stride_b, draft_stride_k;
+  float *out_loss;           // [B][K]
+  void *out_grad;            // [B][K][V] contiguous, or null: the loss alone
+};
+cudaError_t distill_launch(const DistillArgs &a, int dtype_bf16, int reverse, cudaStream_t stream);
+
+// Arguments of the clipping kernels: up to kClipTensors gradients per launch,
+// passed by value in the parameter space (no table to copy to the device).
+constexpr int kClipTensors = 400;
+constexpr float kClipEps = 1e-6f;
+constexpr int kClipPartials = 8192;  // sums of squares of one call (64 KiB of scratch)
+struct ClipArgs {
+  int n;                     // tensors of this launch
+  int partials;              // sums written by all launches of the norm
+  int partial_at;            // where this launch's sums begin
+  float max_norm;
+  int64_t chunks;            // chunks of this launch's tensors
+  double *partial;
+  float *out_norm;           // null except in one launch
+  const void *in[kClipTensors];
+  void *out[kClipTensors];
+  int64_t count[kClipTensors];   // elements
+  int64_t first[kClipTensors];   // the tensor's first chunk
+  uint8_t bf16[kClipTensors];
+};
+int64_t clip_chunks(const void *in, int64_t count, int bf16);
+cudaError_t clip_norm_launch(const ClipArgs &a, int grid, cudaStream_t stream);
+cudaError_t clip_scale_launch(const ClipArgs &a, int grid, cudaStream_t stream);
 
 }  // namespace specv
