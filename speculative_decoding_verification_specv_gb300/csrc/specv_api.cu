@@ -175,7 +175,8 @@ specv_status ensure_device(int *sms_out, int64_t *l2_out) {
         (e = specv::tile_tma_prepare(2 * kTmaTileStageBytes + 16 * 1024)) != cudaSuccess ||
         (e = specv::alpha_prepare()) != cudaSuccess ||
         (e = specv::level_prepare()) != cudaSuccess ||
-        (e = specv::tree_prepare()) != cudaSuccess) {
+        (e = specv::tree_prepare()) != cudaSuccess ||
+        (e = specv::logprobs_prepare()) != cudaSuccess) {
       note_cuda_error(e);
       return SPECV_ERR_CUDA;
     }

@@ -73,8 +73,8 @@ specv_status specv_token_logprobs(const void *logits, const int32_t *tokens, int
   a.stats = reinterpret_cast<float2 *>(out_stats);
   a.top_tokens = out_top_tokens;
   a.top_logprobs = out_top_logprobs;
-  return status_of(
-      specv::logprobs_launch(a, dtype == SPECV_BF16, static_cast<cudaStream_t>(stream)));
+  return status_of(specv::logprobs_launch(a, dtype == SPECV_BF16, sms, specv::cluster_override(),
+                                          static_cast<cudaStream_t>(stream)));
 }
 
 specv_status specv_token_logprobs_backward(const void *logits, const int32_t *tokens,

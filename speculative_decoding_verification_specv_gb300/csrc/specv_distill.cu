@@ -19,19 +19,6 @@ namespace {
 constexpr int kNT = 256;
 
 template <typename T>
-__device__ __forceinline__ T narrow(float x);
-template <>
-__device__ __forceinline__ float narrow<float>(float x) {
-  return x;
-}
-template <>
-__device__ __forceinline__ uint16_t narrow<uint16_t>(float x) {
-  uint16_t h;
-  asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(x));
-  return h;
-}
-
-template <typename T>
 __device__ __forceinline__ float load_plain(const T *p) {
   if constexpr (sizeof(T) == 4)
     return *reinterpret_cast<const float *>(p);

@@ -284,7 +284,10 @@ struct LogprobArgs {
   float *top_logprobs;       // [R][top_n]
 };
 constexpr int kMaxTop = 32;  // one alternative per lane of a warp
-cudaError_t logprobs_launch(const LogprobArgs &a, int dtype_bf16, cudaStream_t stream);
+cudaError_t logprobs_prepare();
+// S: CTAs per row, 0 = the library's choice for a device of `sms` SMs
+cudaError_t logprobs_launch(const LogprobArgs &a, int dtype_bf16, int sms, int S,
+                            cudaStream_t stream);
 
 // Arguments of the log-probability gradient kernel.
 struct LogprobGradArgs {

@@ -6,143 +6,319 @@
 //   log p_x = (z_x - m) - ln S            entropy = ln S - T / S
 // and the top_n largest entries in the order (value falling, index rising),
 // each with its own log probability.
+//
+// The forward kernel reads a row once.  S CTAs (a cluster where S > 1) share a
+// row, each an equal run of its 16-byte vectors; thread t of a CTA takes every
+// NT-th vector of the run: its strip.  The streaming loop keeps S and T about a
+// reference that follows the strip's maximum only when that has risen by more
+// than kLazy, and, of the alternatives, nothing but the strip's maximum and the
+// vector that first held it (two instructions per vector).  After the loop
+//   1. the 32 largest strip maxima over groups of NT / 32 threads are sorted, and
+//      the top_n-th, as the pair (value, vector), is the threshold: at least
+//      top_n entries are no worse, one in each of as many strips;
+//   2. the strips that reach it, about top_n of NT, are read again (L2 still has
+//      them) and their entries that reach it are collected;
+//   3. a warp sorts those and keeps the first top_n.
+// An entry worse than the threshold has top_n better ones, so none is missed; the
+// pair's order makes equal values, a constant row for instance, select top_n
+// strips as well.  Rows that put more than kCand entries above the threshold take
+// a repeated search instead, whose result is the same.
+#include <cooperative_groups.h>
+
+#include "specv_block.cuh"
 #include "specv_internal.h"
 #include "specv_rowstat.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace specv {
 
 namespace {
 
-constexpr int kNT = 256;
+constexpr int kUnroll = 4;      // vectors in flight per thread, and as many being folded
+constexpr int kCand = 512;      // entries collected above the threshold
+// Terms may exceed the reference by e^8: sums stay far from overflow (2^31 e^8 <
+// 10^13), and a strip of ordinary logits moves its reference once or twice.
+constexpr float kLazy = 8.0f;
 
-// Values as whole numbers in the same order (-0 and +0 alike), over the
-// complement of the index: the larger key is the larger value, and among equal
-// values the lower index.  No entry has key 0.
-__device__ __forceinline__ uint64_t order_key(float z, uint32_t index) {
-  uint32_t b = __float_as_uint(__fadd_rn(z, 0.0f));
-  b = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-  return ((uint64_t)b << 32) | (uint32_t)~index;
-}
-__device__ __forceinline__ float key_value(uint64_t key) {
-  const uint32_t b = (uint32_t)(key >> 32);
-  return __uint_as_float((b & 0x80000000u) ? (b & 0x7fffffffu) : ~b);
-}
-__device__ __forceinline__ uint32_t key_index(uint64_t key) { return ~(uint32_t)key; }
+template <int NT, bool CLUSTER>
+struct LogprobShared {
+  float red[NT / 32][3];
+  uint64_t group[32];
+  uint64_t tau;
+  int n_strips, n_cand;
+  int strips[NT];
+  uint64_t cand[kCand];
+  uint64_t best[NT / 32];
+  float4 part[CLUSTER ? kMaxCluster : 1];
+  uint64_t part_top[CLUSTER ? kMaxCluster : 1][kMaxTop];
+};
 
-__device__ __forceinline__ uint64_t shfl_xor_u64(uint64_t x, int off) {
-  return __shfl_xor_sync(0xffffffffu, (unsigned long long)x, off);
+// Running sums of a strip.
+struct StripSums {
+  float ref = -3.402823466e38f;  // the reference of s and t (finite, or +inf)
+  uint64_t s = 0, t = 0;         // packed partial sums
+  float top = -INFINITY;         // the strip's maximum ...
+  int top_vec = 0;               // ... and the first vector that holds it
+};
+
+template <typename T, int U>
+__device__ __forceinline__ void fold(StripSums &a, const uint4 (&v)[U], int k, int step) {
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const float m = vector_max<T>(v[u]);
+    if (m > a.top) {
+      a.top = m;
+      a.top_vec = k + u * step;
+    }
+  }
+  if (a.top > a.ref + kLazy) {
+    const float d = fmaxf(a.ref - a.top, kFarBelow), f = ex2(d * kLog2e);
+    const uint64_t f2 = pack2(f, f);
+    a.t = mul2(f2, fma2(a.s, pack2(d, d), a.t));
+    a.s = mul2(f2, a.s);
+    a.ref = a.top;
+  }
+  const uint64_t neg = pack2(-a.ref, -a.ref), scale = pack2(kLog2e, kLog2e);
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int i = 0; i < Elem<T>::kPerVec / 2; ++i) {
+      const uint64_t d = add2(pair_of<T>(v[u], i), neg);
+      float d0, d1, x0, x1;
+      unpack2(d, d0, d1);
+      unpack2(mul2(d, scale), x0, x1);
+      const uint64_t e = pack2(ex2(x0), ex2(x1));
+      a.s = add2(a.s, e);
+      a.t = fma2(e, pack2(fmaxf(d0, kFarBelow), fmaxf(d1, kFarBelow)), a.t);
+    }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kNT) logprobs_kernel(LogprobArgs a) {
-  __shared__ float red[kNT / 32][3];
-  __shared__ uint64_t best[kNT / 32];
-  const int64_t r = blockIdx.x;
+// The CTA's top_n largest keys among the strips of vectors [lo, hi): lane i of warp
+// 0 returns the i-th.  Every thread calls it.
+template <typename T, int NT, bool CLUSTER>
+__device__ __forceinline__ uint64_t select_top(LogprobShared<NT, CLUSTER> &sh,
+                                               const RowVectors<T> &row, int lo, int hi, int top_n,
+                                               uint64_t strip_key) {
+  constexpr int kGroup = NT / 32;
+  constexpr int VW = Elem<T>::kPerVec;
   const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int V = a.V;
-  const T *row = static_cast<const T *>(a.logits) + row_offset(r, a.N, a.stride_b, a.stride_n);
+  uint64_t key = strip_key;
+#pragma unroll
+  for (int off = kGroup / 2; off > 0; off >>= 1) key = max_u64(key, shfl_xor_u64(key, off));
+  if (tid % kGroup == 0) sh.group[tid / kGroup] = key;
+  if (tid == 0) sh.n_strips = sh.n_cand = 0;
+  __syncthreads();
+  if (warp == 0) {
+    const uint64_t sorted = warp_sort(sh.group[lane]);
+    if (lane == top_n - 1) sh.tau = sorted;
+  }
+  __syncthreads();
+  const uint64_t tau = sh.tau;  // 0: fewer than top_n groups hold an entry, all entries count
+  if (strip_key != 0 && strip_key >= tau) sh.strips[atomicAdd(&sh.n_strips, 1)] = tid;
+  __syncthreads();
+  const float t_value = tau == 0 ? -INFINITY : key_value(tau);
+  const int t_vec = tau == 0 ? -1 : (int)key_index(tau);
+  const int n_strips = sh.n_strips, per_strip = (hi - lo + NT - 1) / NT;
+  for (int64_t i = tid; i < (int64_t)n_strips * per_strip; i += NT) {
+    const int s = (int)(i / per_strip);
+    const int k = lo + sh.strips[s] + (int)(i - (int64_t)s * per_strip) * NT;
+    if (k >= hi) continue;
+    const uint4 v = row.load(k);
+#pragma unroll
+    for (int e = 0; e < VW; ++e) {
+      const float z = Elem<T>::get(v, e);
+      if (z > t_value || (z == t_value && k <= t_vec)) {
+        const int at = atomicAdd(&sh.n_cand, 1);
+        if (at < kCand) sh.cand[at] = order_key(z, (uint32_t)row.index(k, e));
+      }
+    }
+  }
+  __syncthreads();
+  const int n_cand = sh.n_cand;
+  uint64_t top = 0;
+  if (n_cand <= kCand) {
+    if (warp == 0)
+      for (int c = 0; c < n_cand; c += 32) {
+        const uint64_t next = warp_sort(c + lane < n_cand ? sh.cand[c + lane] : 0);
+        top = c == 0 ? next : warp_merge(top, next);
+      }
+    return top;
+  }
+  // the repeated search: the largest key below the last one found
+  uint64_t last = ~0ull;
+  for (int i = 0; i < top_n; ++i) {
+    uint64_t k = 0;
+    for (int64_t j = lo + tid; j < hi; j += NT) {
+      const uint4 v = row.load((int)j);
+#pragma unroll
+      for (int e = 0; e < VW; ++e) {
+        const float z = Elem<T>::get(v, e);
+        const uint64_t c = z > -INFINITY ? order_key(z, (uint32_t)row.index((int)j, e)) : 0;
+        if (c < last && c > k) k = c;
+      }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) k = max_u64(k, shfl_xor_u64(k, off));
+    if (lane == 0) sh.best[warp] = k;
+    __syncthreads();
+    for (int w = 0; w < NT / 32; ++w) k = max_u64(k, sh.best[w]);
+    if (lane == i) top = k;
+    last = k;
+    __syncthreads();
+  }
+  return top;
+}
+
+template <typename T, int NT, bool CLUSTER>
+__global__ void __launch_bounds__(NT, NT == 32 ? 24 : 1024 / NT)
+    logprobs_kernel(LogprobArgs a, int S) {
+  __shared__ LogprobShared<NT, CLUSTER> sh;
+  const int64_t r = CLUSTER ? (int64_t)blockIdx.x / S : (int64_t)blockIdx.x;
+  const int rank = CLUSTER ? (int)cg::this_cluster().block_rank() : 0;
+  const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int V = a.V, top_n = a.top_n;
   const int32_t x = a.tokens[r];
   if (x < 0 || x >= V) {  // no token (-1): the row is not read; an invalid one: NaN
+    if (rank != 0) return;
     const float fill = x == -1 ? 0.0f : quiet_nan();
     if (tid == 0) {
       a.logprob[r] = fill;
       a.entropy[r] = fill;
       a.stats[r] = make_float2(fill, fill);
     }
-    for (int i = tid; i < a.top_n; i += kNT) {
-      a.top_tokens[r * a.top_n + i] = -1;
-      a.top_logprobs[r * a.top_n + i] = x == -1 ? -INFINITY : quiet_nan();
+    for (int i = tid; i < top_n; i += NT) {
+      a.top_tokens[r * top_n + i] = -1;
+      a.top_logprobs[r * top_n + i] = x == -1 ? -INFINITY : quiet_nan();
     }
     return;
   }
-  float m = -INFINITY, s = 0.0f, t = 0.0f;
-  for (int64_t v = tid; v < V; v += kNT) {
-    const float z = Elem<T>::load(row + v);
-    if (z > m) {
-      const float d = fmaxf(m - z, kFarBelow), f = ex2(d * kLog2e);
-      t = f * (t + s * d);
-      s *= f;
-      m = z;
+  if (CLUSTER) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  const T *first = static_cast<const T *>(a.logits) + row_offset(r, a.N, a.stride_b, a.stride_n);
+  const RowVectors<T> row(first, V);
+  const int per = (row.count + S - 1) / S;
+  const int lo = min(row.count, rank * per), hi = min(row.count, lo + per);
+  const float zx = rank == 0 && tid == 0 ? Elem<T>::load(first + x) : 0.0f;
+
+  // -------------------------------------------------- the strip's sums and maximum
+  StripSums sums;
+  constexpr int kBatch = NT * kUnroll;
+  constexpr uint32_t none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+  const int plain_hi = min(hi, row.full_hi);
+  auto load_batch = [&](int base, uint4 (&v)[kUnroll]) {
+    if (base >= row.full_lo && base <= plain_hi - kBatch) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) v[u] = row.load_full(base + u * NT + tid);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int k = base + u * NT + tid;
+        v[u] = make_uint4(none, none, none, none);
+        if (k < hi) v[u] = row.load(k);
+      }
     }
-    const float d = z - (m == -INFINITY ? 0.0f : m), e = ex2(d * kLog2e);
-    s += e;
-    t = __fmaf_rn(e, fmaxf(d, kFarBelow), t);
+  };
+  uint4 cur[kUnroll], next[kUnroll];
+  load_batch(lo, cur);
+  for (int base = lo; base < hi; base += kBatch) {
+    const bool more = hi - base > kBatch;
+    if (more) load_batch(base + kBatch, next);
+    fold<T, kUnroll>(sums, cur, base + tid, NT);
+    if (more) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) cur[u] = next[u];
+    }
   }
-  // merge: the maximum first, then every partial recentred on it
-  float M = m;
+
+  // ------------------------------------------------------------------ merge: the CTA
+  float M = sums.top, s, t, s1, t1;
+  unpack2(sums.s, s, s1);
+  unpack2(sums.t, t, t1);
+  s += s1;
+  t += t1;
+#pragma unroll
   for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, off));
-  if (lane == 0) red[warp][0] = M;
-  __syncthreads();
-  for (int w = 0; w < kNT / 32; ++w) M = fmaxf(M, red[w][0]);
-  if (s == 0.0f) {
-    t = 0.0f;
-  } else {
-    const float d = fmaxf(m - M, kFarBelow), f = ex2(d * kLog2e);
-    t = f * (t + s * d);
-    s *= f;
-  }
+  recentre(sums.ref, M, s, t);
+#pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
     s += __shfl_xor_sync(~0u, s, off);
     t += __shfl_xor_sync(~0u, t, off);
   }
   if (lane == 0) {
-    red[warp][1] = s;
-    red[warp][2] = t;
+    sh.red[warp][0] = M;
+    sh.red[warp][1] = s;
+    sh.red[warp][2] = t;
   }
-  __syncthreads();
-  float S = 0.0f, Tw = 0.0f;
-  for (int w = 0; w < kNT / 32; ++w) {
-    S += red[w][1];
-    Tw += red[w][2];
-  }
-  const bool bad = !(S < INFINITY);  // a NaN or +inf entry
-  const bool none = !bad && M == -INFINITY;
-  const float ln = logf(S);
-  if (tid == 0) {
-    const float z = Elem<T>::load(row + x);
-    a.logprob[r] = bad ? quiet_nan() : none ? -INFINITY : (z - M) - ln;
-    a.entropy[r] = bad ? quiet_nan() : none ? 0.0f : fmaxf(ln - Tw / S, 0.0f);
-    a.stats[r] = bad ? make_float2(quiet_nan(), quiet_nan())
-                     : make_float2(M, none ? 0.0f : ln);
-  }
-  // the alternatives: the largest key below the last one found
-  uint64_t last = ~0ull;
-  for (int i = 0; i < a.top_n; ++i) {
-    uint64_t k = 0;
-    for (int64_t v = tid; v < V; v += kNT) {
-      const float z = Elem<T>::load(row + v);
-      const uint64_t c = z > -INFINITY ? order_key(z, (uint32_t)v) : 0;
-      if (c < last && c > k) k = c;
-    }
-    for (int off = 16; off > 0; off >>= 1) {
-      const uint64_t o = shfl_xor_u64(k, off);
-      k = o > k ? o : k;
-    }
+  uint64_t top = 0;  // lane i of warp 0: the i-th largest key
+  if (top_n > 0)
+    top = select_top<T>(sh, row, lo, hi, top_n,
+                        sums.top > -INFINITY ? order_key(sums.top, (uint32_t)sums.top_vec) : 0);
+  else
     __syncthreads();
-    if (lane == 0) best[warp] = k;
-    __syncthreads();
-    for (int w = 0; w < kNT / 32; ++w) k = best[w] > k ? best[w] : k;
-    if (tid == 0) {
-      a.top_tokens[r * a.top_n + i] = bad || k == 0 ? -1 : (int32_t)key_index(k);
-      a.top_logprobs[r * a.top_n + i] =
-          bad ? quiet_nan() : k == 0 ? -INFINITY : (key_value(k) - M) - ln;
+  if (warp == 0) {
+    constexpr int kNW = NT / 32;
+    M = lane < kNW ? sh.red[lane][0] : -INFINITY;
+    s = lane < kNW ? sh.red[lane][1] : 0.0f;
+    t = lane < kNW ? sh.red[lane][2] : 0.0f;
+    const float m = M;
+#pragma unroll
+    for (int off = kNW / 2; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, off));
+    M = __shfl_sync(~0u, M, 0);
+    recentre(m, M, s, t);
+#pragma unroll
+    for (int off = kNW / 2; off > 0; off >>= 1) {
+      s += __shfl_xor_sync(~0u, s, off);
+      t += __shfl_xor_sync(~0u, t, off);
     }
-    last = k;
+  }
+
+  // -------------------------------------------------------------- merge: the cluster
+  if (CLUSTER) {
+    cg::cluster_group cluster = cg::this_cluster();
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA has begun
+    if (warp == 0) {
+      if (lane == 0) *cluster.map_shared_rank(&sh.part[rank], 0) = make_float4(M, s, t, 0.0f);
+      if (lane < top_n) *cluster.map_shared_rank(&sh.part_top[rank][lane], 0) = top;
+    }
+    cluster.sync();
+    if (rank != 0) return;
+    if (warp == 0) {
+      const float4 p = lane < S ? sh.part[lane] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+      M = p.x;
+      s = p.y;
+      t = p.z;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, off));
+      recentre(p.x, M, s, t);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) {
+        s += __shfl_xor_sync(~0u, s, off);
+        t += __shfl_xor_sync(~0u, t, off);
+      }
+      if (top_n > 0)
+        for (int q = 1; q < S; ++q) top = warp_merge(top, lane < top_n ? sh.part_top[q][lane] : 0);
+    }
+  }
+  if (warp != 0) return;
+  s = __shfl_sync(~0u, s, 0);
+  t = __shfl_sync(~0u, t, 0);
+  const bool bad = !(s < INFINITY);  // a NaN or +inf entry
+  const bool empty = !bad && M == -INFINITY;
+  const float ln = logf(s);
+  if (lane == 0) {
+    a.logprob[r] = bad ? quiet_nan() : empty ? -INFINITY : (zx - M) - ln;
+    a.entropy[r] = bad ? quiet_nan() : empty ? 0.0f : fmaxf(ln - t / s, 0.0f);
+    a.stats[r] = bad ? make_float2(quiet_nan(), quiet_nan()) : make_float2(M, empty ? 0.0f : ln);
+  }
+  if (lane < top_n) {
+    const bool some = !bad && top != 0;
+    a.top_tokens[r * top_n + lane] = some ? (int32_t)key_index(top) : -1;
+    a.top_logprobs[r * top_n + lane] =
+        bad ? quiet_nan() : some ? (key_value(top) - M) - ln : -INFINITY;
   }
 }
 
-template <typename T>
-__device__ __forceinline__ T narrow(float x);
-template <>
-__device__ __forceinline__ float narrow<float>(float x) {
-  return x;
-}
-template <>
-__device__ __forceinline__ uint16_t narrow<uint16_t>(float x) {
-  uint16_t h;
-  asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(x));
-  return h;
-}
+constexpr int kNT = 256;
 
 // dz_v = g (1[v = x] - p_v) - h p_v (ln p_v + H): one CTA per row.
 template <typename T>
@@ -170,14 +346,52 @@ __global__ void __launch_bounds__(kNT) logprobs_grad_kernel(LogprobGradArgs a) {
   }
 }
 
+template <typename T, int NT, bool CLUSTER>
+cudaError_t launch_forward(const LogprobArgs &a, int S, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.R * S), 1, 1);
+  cfg.blockDim = dim3(NT, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)S;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CLUSTER ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, NT, CLUSTER>, a, S);
+}
+
+template <typename T>
+cudaError_t forward(const LogprobArgs &a, int sms, int S, cudaStream_t stream) {
+  constexpr int kVW = Elem<T>::kPerVec;
+  const int64_t vectors = (a.V + kVW - 1) / kVW;
+  // Short rows: a warp per row, up to 8 vectors per lane.
+  if (S == 0 && vectors <= 32 * 8) return launch_forward<T, 32, false>(a, 1, stream);
+  // CTAs per row: enough for two per SM, each with a batch of vectors at least.
+  if (S == 0) {
+    S = 1;
+    while (S < kMaxCluster && a.R * S < 2 * sms && vectors / (2 * S) >= 256 * kUnroll / 2) S *= 2;
+  }
+  while (S > 1 && a.R * S > INT32_MAX) S /= 2;
+  return S == 1 ? launch_forward<T, 256, false>(a, 1, stream)
+                : launch_forward<T, 256, true>(a, S, stream);
+}
+
 }  // namespace
 
-cudaError_t logprobs_launch(const LogprobArgs &a, int dtype_bf16, cudaStream_t stream) {
-  if (dtype_bf16)
-    logprobs_kernel<uint16_t><<<(unsigned)a.R, kNT, 0, stream>>>(a);
-  else
-    logprobs_kernel<float><<<(unsigned)a.R, kNT, 0, stream>>>(a);
-  return cudaGetLastError();
+cudaError_t logprobs_prepare() {
+  cudaError_t e = cudaFuncSetAttribute(logprobs_kernel<float, 256, true>,
+                                       cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(logprobs_kernel<uint16_t, 256, true>,
+                             cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  return e;
+}
+
+cudaError_t logprobs_launch(const LogprobArgs &a, int dtype_bf16, int sms, int S,
+                            cudaStream_t stream) {
+  return dtype_bf16 ? forward<uint16_t>(a, sms, S, stream) : forward<float>(a, sms, S, stream);
 }
 
 cudaError_t logprobs_grad_launch(const LogprobGradArgs &a, int dtype_bf16, cudaStream_t stream) {
