@@ -527,8 +527,10 @@ typedef enum {
  *
  * An entry whose leading probability (p_t forward, q reverse) is zero in fp32
  * adds nothing.  An entry of positive leading probability that the other row
- * masks (-inf) makes the loss +inf; the forward gradient weight * (q - p_t) is
- * still written, the reverse gradient is NaN at every entry of positive q.  A
+ * masks (-inf) makes the loss +inf (certain where its leading logit lies within 87
+ * of the row's largest, open down to 175 below it); the forward gradient
+ * weight * (q - p_t) is still written, the reverse gradient is NaN at every entry
+ * of positive q.  A
  * pair in which either row masks every entry has no divergence: loss 0, gradient
  * 0.  A NaN or +inf logit gives NaN for its pair.  Sums are fp32; a loss below
  * zero by rounding is written as 0.  No scratch, no allocation; asynchronous on

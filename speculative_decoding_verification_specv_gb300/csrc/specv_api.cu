@@ -176,7 +176,8 @@ specv_status ensure_device(int *sms_out, int64_t *l2_out) {
         (e = specv::alpha_prepare()) != cudaSuccess ||
         (e = specv::level_prepare()) != cudaSuccess ||
         (e = specv::tree_prepare()) != cudaSuccess ||
-        (e = specv::logprobs_prepare()) != cudaSuccess) {
+        (e = specv::logprobs_prepare()) != cudaSuccess ||
+        (e = specv::distill_prepare()) != cudaSuccess) {
       note_cuda_error(e);
       return SPECV_ERR_CUDA;
     }

@@ -140,7 +140,7 @@ specv_status specv_distill(const void *target_logits, const void *draft_logits,
   a.out_loss = out_loss;
   a.out_grad = out_grad;
   return status_of(specv::distill_launch(a, dtype == SPECV_BF16, kind == SPECV_REVERSE_KL,
-                                         static_cast<cudaStream_t>(stream)));
+                                         specv::cluster_override(), static_cast<cudaStream_t>(stream)));
 }
 
 specv_status specv_clip_grads(const specv_grad *grads, int64_t n, float max_norm, float *out_norm,

@@ -317,7 +317,10 @@ struct DistillArgs {
   float *out_loss;           // [B][K]
   void *out_grad;            // [B][K][V] contiguous, or null: the loss alone
 };
-cudaError_t distill_launch(const DistillArgs &a, int dtype_bf16, int reverse, cudaStream_t stream);
+cudaError_t distill_prepare();
+// S: CTAs per row pair, 0 = the library's choice
+cudaError_t distill_launch(const DistillArgs &a, int dtype_bf16, int reverse, int S,
+                           cudaStream_t stream);
 
 // Arguments of the clipping kernels: up to kClipTensors gradients per launch,
 // passed by value in the parameter space (no table to copy to the device).
