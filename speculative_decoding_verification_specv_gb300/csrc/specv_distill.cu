@@ -27,126 +27,7 @@ namespace specv {
 
 namespace {
 
-constexpr int kRegs = 16;   // registers per thread that hold a row's entries
-constexpr float kLazy = 8.0f;
-
-// W consecutive entries of a row in registers, read and written as one access of
-// W * sizeof(T) bytes; entry pairs are widened as they are used.
-template <typename T, int W>
-struct Pack;
-template <typename T>
-struct Pack<T, 16 / sizeof(T)> {
-  static constexpr int kRegsEach = 4;
-  uint4 v;
-  __device__ __forceinline__ void none() {
-    constexpr uint32_t n = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
-    v = make_uint4(n, n, n, n);
-  }
-  __device__ __forceinline__ void load(const T *p) {
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-  }
-  __device__ __forceinline__ uint64_t pair(int i) const { return pair_of<T>(v, i); }
-  __device__ __forceinline__ float largest() const { return vector_max<T>(v); }
-  // the same registers take the gradient's entries, pair by pair
-  __device__ __forceinline__ void put(int i, float a, float b) {
-    if constexpr (sizeof(T) == 2) {
-      uint32_t &w = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
-    } else if (i == 0) {
-      v.x = __float_as_uint(a);
-      v.y = __float_as_uint(b);
-    } else {
-      v.z = __float_as_uint(a);
-      v.w = __float_as_uint(b);
-    }
-  }
-  __device__ __forceinline__ void store(T *p) const { *reinterpret_cast<uint4 *>(p) = v; }
-};
-template <>
-struct Pack<uint16_t, 2> {
-  static constexpr int kRegsEach = 1;
-  uint32_t v;
-  __device__ __forceinline__ void none() { v = 0xff80ff80u; }
-  __device__ __forceinline__ void load(const uint16_t *p) {
-    asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(v) : "l"(p));
-  }
-  __device__ __forceinline__ uint64_t pair(int) const {
-    return pack2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
-  }
-  __device__ __forceinline__ float largest() const {
-    return fmaxf(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
-  }
-  __device__ __forceinline__ void put(int, float a, float b) {
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(b), "f"(a));
-  }
-  __device__ __forceinline__ void store(uint16_t *p) const { *reinterpret_cast<uint32_t *>(p) = v; }
-};
-// single entries, widened on load
-template <typename T>
-struct Single {
-  float v;
-  __device__ __forceinline__ void none() { v = -INFINITY; }
-  __device__ __forceinline__ void load(const T *p) {
-    if constexpr (sizeof(T) == 2) {
-      uint16_t h;
-      asm volatile("ld.global.L1::no_allocate.u16 %0, [%1];" : "=h"(h) : "l"(p));
-      v = bf16_bits_to_float(h);
-    } else {
-      asm volatile("ld.global.L1::no_allocate.f32 %0, [%1];" : "=f"(v) : "l"(p));
-    }
-  }
-  __device__ __forceinline__ void store(T *p) const { *p = narrow<T>(v); }
-};
-
-// A tile: a thread's entries of one row.  Access j covers entries
-// ((j * NT) + tid) * W onwards of the tile; pairs(f) calls f(register-pair index)
-// over packed pairs whatever W is.
-template <typename T, int W, int NT>
-struct Tile {
-  static constexpr int kAccesses = kRegs / Pack<T, W>::kRegsEach;
-  static constexpr int kPairsEach = W / 2;
-  static constexpr int kPairs = kAccesses * kPairsEach;
-  static constexpr int kEntries = kAccesses * W;  // per thread
-  Pack<T, W> a[kAccesses];
-  __device__ __forceinline__ void load(int j, const T *p) { a[j].load(p); }
-  __device__ __forceinline__ void none(int j) { a[j].none(); }
-  __device__ __forceinline__ void store(int j, T *p) const { a[j].store(p); }
-  __device__ __forceinline__ uint64_t pair(int i) const {
-    return a[i / kPairsEach].pair(i % kPairsEach);
-  }
-  __device__ __forceinline__ void put(int i, float x, float y) {
-    a[i / kPairsEach].put(i % kPairsEach, x, y);
-  }
-  __device__ __forceinline__ float largest() const {
-    float m = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < kAccesses; ++j) m = fmaxf(m, a[j].largest());
-    return m;
-  }
-};
-template <typename T, int NT>
-struct Tile<T, 1, NT> {
-  static constexpr int kAccesses = kRegs;
-  static constexpr int kPairs = kRegs / 2;
-  static constexpr int kEntries = kRegs;
-  Single<T> a[kAccesses];
-  __device__ __forceinline__ void load(int j, const T *p) { a[j].load(p); }
-  __device__ __forceinline__ void none(int j) { a[j].none(); }
-  __device__ __forceinline__ void store(int j, T *p) const { a[j].store(p); }
-  __device__ __forceinline__ uint64_t pair(int i) const { return pack2(a[2 * i].v, a[2 * i + 1].v); }
-  __device__ __forceinline__ void put(int i, float x, float y) {
-    a[2 * i].v = x;
-    a[2 * i + 1].v = y;
-  }
-  __device__ __forceinline__ float largest() const {
-    float m = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < kAccesses; ++j) m = fmaxf(m, a[j].v);
-    return m;
-  }
-};
+constexpr float kLazy = 8.0f;   // what a term may exceed its reference by, as a power of e
 
 // Partial sums of a row pair about the references (rt, rq).
 struct PairSums {
@@ -171,117 +52,381 @@ __device__ __forceinline__ void move_to(PairSums &x, float Mt, float Mq) {
   x.rq = Mq;
 }
 
-template <int NT>
-struct DistillShared {
-  float4 a[kMaxCluster * (NT / 32)];  // (rt, st, rq, sq) of every warp of the cluster
-  float t[kMaxCluster * (NT / 32)];
+// ------------------------------------------------------------------ shared steps
+struct Merged {
+  float lt, lq;  // ln S of the target's and the draft's row
+  float rt, rq;  // their references
+  float kl;      // the divergence: NaN for a row with a NaN or +inf
+  bool empty;    // a row masks every entry
 };
 
-template <typename T, int W, int NT, bool REVERSE>
-__global__ void __launch_bounds__(NT, 768 / NT) distill_kernel(DistillArgs a, int S) {
-  using TileT = Tile<T, W, NT>;
-  constexpr int kNW = NT / 32;
-  __shared__ DistillShared<NT> sh;
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = S > 1 ? (int)cluster.block_rank() : 0;
-  const int64_t r = (int64_t)blockIdx.x / S;
+template <bool REVERSE>
+__device__ __forceinline__ void merge_lanes(PairSums &y) {
+  float Mt = y.rt, Mq = y.rq;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    Mt = fmaxf(Mt, __shfl_xor_sync(~0u, Mt, off));
+    Mq = fmaxf(Mq, __shfl_xor_sync(~0u, Mq, off));
+  }
+  move_to<REVERSE>(y, Mt, Mq);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    y.st += __shfl_xor_sync(~0u, y.st, off);
+    y.sq += __shfl_xor_sync(~0u, y.sq, off);
+    y.t += __shfl_xor_sync(~0u, y.t, off);
+  }
+}
+
+// The partials of `parts` warps (a: rt, st, rq, sq), merged by a warp; every lane
+// returns the same.
+template <bool REVERSE>
+__device__ __forceinline__ Merged merge_parts(const float4 *a, const float *t, int parts) {
+  const int lane = threadIdx.x & 31;
+  PairSums y;
+  for (int i = lane; i < parts; i += 32) {
+    y.rt = fmaxf(y.rt, a[i].x);
+    y.rq = fmaxf(y.rq, a[i].z);
+  }
+  for (int i = lane; i < parts; i += 32) {
+    PairSums z;
+    z.rt = a[i].x;
+    z.st = a[i].y;
+    z.rq = a[i].z;
+    z.sq = a[i].w;
+    z.t = t[i];
+    move_to<REVERSE>(z, y.rt, y.rq);
+    y.st += z.st;
+    y.sq += z.sq;
+    y.t += z.t;
+  }
+  merge_lanes<REVERSE>(y);
+  Merged m;
+  const bool bad = !(y.st < INFINITY) || !(y.sq < INFINITY);
+  m.empty = !bad && (y.st == 0.0f || y.sq == 0.0f);
+  m.lt = logf(y.st);
+  m.lq = logf(y.sq);
+  m.rt = y.rt;
+  m.rq = y.rq;
+  const float kl = REVERSE ? y.t / y.sq - m.lq + m.lt : y.t / y.st - m.lt + m.lq;
+  m.kl = bad ? quiet_nan() : kl < 0.0f ? 0.0f : kl;
+  return m;
+}
+
+// Adds the entries of two tiles to the sums.
+template <typename T, bool REVERSE, typename TileT>
+__device__ __forceinline__ void fold_pair(PairSums &x, const TileT &xt, const TileT &xq) {
+  const float mt = xt.largest(), mq = xq.largest();
+  if (mt > x.rt + kLazy || mq > x.rq + kLazy)
+    move_to<REVERSE>(x, fmaxf(x.rt, mt), fmaxf(x.rq, mq));
+  const uint64_t nt = pack2(-x.rt, -x.rt), nq = pack2(-x.rq, -x.rq);
+  const uint64_t scale = pack2(kLog2e, kLog2e), minus = pack2(-1.0f, -1.0f);
+  uint64_t st = 0, sq = 0;
+  float t0 = 0.0f, t1 = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kTilePairs<T>; ++i) {
+    const uint64_t dt = add2(xt.pair(i), nt), dq = add2(xq.pair(i), nq);
+    float a0, a1, b0, b1, d0, d1;
+    unpack2(mul2(dt, scale), a0, a1);
+    unpack2(mul2(dq, scale), b0, b1);
+    a0 = ex2(a0);
+    a1 = ex2(a1);
+    b0 = ex2(b0);
+    b1 = ex2(b1);
+    st = add2(st, pack2(a0, a1));
+    sq = add2(sq, pack2(b0, b1));
+    unpack2(REVERSE ? fma2(dt, minus, dq) : fma2(dq, minus, dt), d0, d1);
+    // an entry without leading probability adds nothing (its difference may be
+    // infinite or NaN); one with it against a masked entry adds +inf
+    const float e0 = REVERSE ? b0 : a0, e1 = REVERSE ? b1 : a1;
+    if (e0 > 0.0f) t0 = __fmaf_rn(e0, d0, t0);
+    if (e1 > 0.0f) t1 = __fmaf_rn(e1, d1, t1);
+  }
+  float s0, s1;
+  unpack2(st, s0, s1);
+  x.st += s0 + s1;
+  unpack2(sq, s0, s1);
+  x.sq += s0 + s1;
+  x.t += t0 + t1;
+}
+
+// What the gradient needs of a row pair, in packed pairs.
+struct GradTerms {
+  uint64_t rt, rq;  // -r
+  uint64_t lt, lq;  // -log2 S
+  uint64_t w, c;
+  bool bad;
+  __device__ __forceinline__ GradTerms(const Merged &m, float weight) {
+    bad = m.kl != m.kl;
+    const float wg = bad ? quiet_nan() : weight;
+    const float cc = m.kl == INFINITY ? quiet_nan() : m.lt - m.lq - m.kl;
+    rt = pack2(-m.rt, -m.rt);
+    rq = pack2(-m.rq, -m.rq);
+    lt = pack2(-m.lt * kLog2e, -m.lt * kLog2e);
+    lq = pack2(-m.lq * kLog2e, -m.lq * kLog2e);
+    w = pack2(wg, wg);
+    c = pack2(cc, cc);
+  }
+};
+
+// Puts the gradient of the entries of xt and xq into xq.
+template <typename T, bool REVERSE, typename TileT>
+__device__ __forceinline__ void gradient(const GradTerms &g, const TileT &xt, TileT &xq) {
+  const uint64_t scale = pack2(kLog2e, kLog2e), minus = pack2(-1.0f, -1.0f);
+#pragma unroll
+  for (int i = 0; i < kTilePairs<T>; ++i) {
+    const uint64_t dt = add2(xt.pair(i), g.rt), dq = add2(xq.pair(i), g.rq);
+    float q0, q1, g0, g1;
+    unpack2(fma2(dq, scale, g.lq), q0, q1);
+    q0 = ex2(q0);
+    q1 = ex2(q1);
+    if (REVERSE) {
+      unpack2(mul2(mul2(g.w, pack2(q0, q1)), add2(fma2(dt, minus, dq), g.c)), g0, g1);
+      if (q0 == 0.0f) g0 = 0.0f;
+      if (q1 == 0.0f) g1 = 0.0f;
+      if (g.bad) g0 = g1 = quiet_nan();
+    } else {
+      float p0, p1;
+      unpack2(fma2(dt, scale, g.lt), p0, p1);
+      unpack2(mul2(g.w, fma2(pack2(ex2(p0), ex2(p1)), minus, pack2(q0, q1))), g0, g1);
+    }
+    xq.put(i, g0, g1);
+  }
+}
+
+// ------------------------------------------------------------------- short rows
+// One CTA of 64 threads per pair, at most two register tiles of it.
+constexpr int kSmallNT = 64;
+
+template <typename T, bool SHIFTED, bool REVERSE>
+__global__ void __launch_bounds__(kSmallNT) distill_short_kernel(DistillArgs a) {
+  constexpr int kNW = kSmallNT / 32;
+  __shared__ float4 part_a[kNW];
+  __shared__ float part_t[kNW];
+  const int64_t r = blockIdx.x;
   const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int V = a.V;
   const T *zt =
       static_cast<const T *>(a.target) + row_offset(r, a.K, a.target_stride_b, a.target_stride_k);
   const T *zq =
       static_cast<const T *>(a.draft) + row_offset(r, a.K, a.draft_stride_b, a.draft_stride_k);
-  T *out = a.out_grad == nullptr ? nullptr : static_cast<T *>(a.out_grad) + r * (int64_t)V;
-  // this CTA's accesses [lo, hi) of W entries, in tiles (V is a multiple of W)
-  const int n = V / W, per = (n + S - 1) / S;
-  const int lo = min(n, rank * per), hi = min(n, lo + per);
-  constexpr int kTile = TileT::kAccesses * NT;
-  const int tiles = (hi - lo + kTile - 1) / kTile;
+  T *out = a.out_grad == nullptr ? nullptr : static_cast<T *>(a.out_grad) + r * (int64_t)a.V;
+  const Grid<T> grid(out != nullptr ? static_cast<const void *>(out) : zq, a.V);
   const float w = a.weight == nullptr ? 1.0f : a.weight[r];
-
-  TileT xt, xq;
   auto zero_fill = [&]() {
     if (out == nullptr) return;
+    for (int k = tid; k < grid.count; k += kSmallNT)
+      store_pack<T>(out, grid, k, make_uint4(0, 0, 0, 0));
+  };
+  if (w == 0.0f) {
+    if (tid == 0) a.out_loss[r] = 0.0f;
+    zero_fill();
+    return;
+  }
+  const GridRow<T, SHIFTED> rt(zt, grid), rq(zq, grid);
+  constexpr int kTile = kPackUnroll * kSmallNT;
+  PackTile<T, SHIFTED> xt[2], xq[2];
+  PairSums x;
 #pragma unroll
-    for (int i = 0; i < TileT::kPairs; ++i) xq.put(i, 0.0f, 0.0f);
-    for (int k = lo + tid; k < hi; k += NT) xq.store(0, out + (int64_t)k * W);
+  for (int i = 0; i < 2; ++i) {
+    xt[i].load(rt, grid, i * kTile + warp * 32 * kPackUnroll, grid.count);
+    xq[i].load(rq, grid, i * kTile + warp * 32 * kPackUnroll, grid.count);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    xt[i].join(rt);
+    xq[i].join(rq);
+    fold_pair<T, REVERSE>(x, xt[i], xq[i]);
+  }
+  merge_lanes<REVERSE>(x);
+  if (lane == 0) {
+    part_a[warp] = make_float4(x.rt, x.st, x.rq, x.sq);
+    part_t[warp] = x.t;
+  }
+  __syncthreads();
+  const Merged m = merge_parts<REVERSE>(part_a, part_t, kNW);
+  if (tid == 0) a.out_loss[r] = m.empty ? 0.0f : w * m.kl;
+  if (out == nullptr) return;
+  if (m.empty) {
+    zero_fill();
+    return;
+  }
+  const GradTerms g(m, w);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    gradient<T, REVERSE>(g, xt[i], xq[i]);
+#pragma unroll
+    for (int j = 0; j < kPackUnroll; ++j) {
+      const int k = i * kTile + (warp * kPackUnroll + j) * 32 + lane;
+      if (k < grid.count) store_pack<T>(out, grid, k, xq[i].v[j]);
+    }
+  }
+}
+
+// -------------------------------------------------------------------- long rows
+constexpr int kNT = 256;            // consuming threads; one more warp issues the copies
+constexpr int kChunk = kNT * kPackUnroll;          // packs of a chunk
+constexpr int kChunkBytes = (kChunk + 1) * 16;     // a shifted row's chunk needs one vector more
+constexpr int kBuffers = 4;                        // chunks of both rows held per CTA
+
+struct __align__(16) DistillShared {
+  float4 a[kMaxCluster * (kNT / 32)];  // (rt, st, rq, sq) of every warp of the cluster
+  float t[kMaxCluster * (kNT / 32)];
+  uint64_t full[kBuffers], empty[kBuffers];
+  int lost;  // set when a copy did not land in time
+};
+
+// A thread's packs of a chunk, read from shared memory (edge packs from the row).
+template <typename T, bool SHIFTED>
+struct ChunkTile {
+  uint4 v[kPackUnroll];
+  __device__ __forceinline__ void load(const GridRow<T, SHIFTED> &r, const Grid<T> &grid,
+                                       const uint4 *buf, int k0, int end) {
+    constexpr int VW = Elem<T>::kPerVec;
+#pragma unroll
+    for (int j = 0; j < kPackUnroll; ++j) {
+      const int i = j * kNT + (int)threadIdx.x, k = k0 + i;
+      if (!SHIFTED) {
+        v[j] = k < end ? buf[i] : PackTile<T, false>::none();
+      } else if (k >= r.lo && k < min(r.hi, end)) {
+        v[j] = buf[i];
+        if (r.shift != 0) v[j] = shifted<T>(v[j], buf[i + 1], r.shift);
+      } else {
+        v[j] = PackTile<T, true>::none();
+        if (k < end) v[j] = PackTile<T, true>::load_entries(r.row, (int64_t)k * VW - grid.mis, grid.V);
+      }
+    }
+  }
+  __device__ __forceinline__ uint64_t pair(int i) const {
+    constexpr int kEach = Elem<T>::kPerVec / 2;
+    return pair_of<T>(v[i / kEach], i % kEach);
+  }
+  __device__ __forceinline__ float largest() const {
+    float m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < kPackUnroll; ++j) m = fmaxf(m, vector_max<T>(v[j]));
+    return m;
+  }
+  __device__ __forceinline__ void put(int i, float a, float b) {
+    constexpr int kEach = Elem<T>::kPerVec / 2;
+    put_pair<T>(v[i / kEach], i % kEach, a, b);
+  }
+};
+
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+template <typename T, bool SHIFTED, bool REVERSE>
+__global__ void __launch_bounds__(kNT + 32, 3) distill_kernel(DistillArgs a, int S) {
+  constexpr int kNW = kNT / 32;
+  extern __shared__ __align__(16) unsigned char chunks[];  // [kBuffers][2][kChunkBytes]
+  __shared__ DistillShared sh;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = S > 1 ? (int)cluster.block_rank() : 0;
+  const int64_t r = (int64_t)blockIdx.x / S;
+  const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const T *zt =
+      static_cast<const T *>(a.target) + row_offset(r, a.K, a.target_stride_b, a.target_stride_k);
+  const T *zq =
+      static_cast<const T *>(a.draft) + row_offset(r, a.K, a.draft_stride_b, a.draft_stride_k);
+  T *out = a.out_grad == nullptr ? nullptr : static_cast<T *>(a.out_grad) + r * (int64_t)a.V;
+  // the packs of the gradient's row (of the draft's where none is wanted)
+  const Grid<T> grid(out != nullptr ? static_cast<const void *>(out) : zq, a.V);
+  const int per = (grid.count + S - 1) / S;
+  const int lo = min(grid.count, rank * per), hi = min(grid.count, lo + per);
+  const int n = (hi - lo + kChunk - 1) / kChunk;  // chunks of this CTA
+  const float w = a.weight == nullptr ? 1.0f : a.weight[r];
+
+  auto zero_fill = [&]() {  // by the consuming threads
+    if (out == nullptr || warp == kNW) return;
+    for (int k = lo + tid; k < hi; k += kNT) store_pack<T>(out, grid, k, make_uint4(0, 0, 0, 0));
   };
   if (w == 0.0f) {
     if (rank == 0 && tid == 0) a.out_loss[r] = 0.0f;
     zero_fill();
     return;
   }
-  if (S > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-
-  auto load_tile = [&](int tile) {
-    const int base = lo + tile * kTile + tid;
-#pragma unroll
-    for (int j = 0; j < TileT::kAccesses; ++j) {
-      const int k = base + j * NT;
-      if (k < hi) {
-        xt.load(j, zt + (int64_t)k * W);
-        xq.load(j, zq + (int64_t)k * W);
-      } else {
-        xt.none(j);
-        xq.none(j);
-      }
+  if (tid == 0) {
+    sh.lost = 0;
+    for (int b = 0; b < kBuffers; ++b) {
+      mbar_init(&sh.full[b], 1);
+      mbar_init(&sh.empty[b], kNW);
     }
+    mbar_fence_init();
+  }
+  if (S > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  __syncthreads();
+
+  const GridRow<T, SHIFTED> rt(zt, grid), rq(zq, grid);
+  auto buffer = [&](int c, int which) {
+    return reinterpret_cast<uint4 *>(chunks + ((c % kBuffers) * 2 + which) * kChunkBytes);
+  };
+  // Chunk c goes to buffer c mod kBuffers.  The copies run 0 .. n-1 for pass 1, then
+  // n-kBuffers-1 .. 0 for pass 2, which begins with the chunks still held.  The m-th
+  // copy into a buffer completes phase m of its `full` barrier and waits for phase
+  // m-1 of its `empty` one.  `loads` of a chunk: m in pass 1, and in pass 2.
+  auto load_1 = [&](int c) { return c / kBuffers; };
+  auto load_2 = [&](int c) {
+    const int held = (n - 1 - c % kBuffers) / kBuffers;  // copies before the held chunk's
+    return held + (held - c / kBuffers);
   };
 
-  // ------------------------------------------------------------- pass 1: the sums
-  PairSums x;
-  const uint64_t scale = pack2(kLog2e, kLog2e), minus = pack2(-1.0f, -1.0f);
-  for (int tile = 0; tile < tiles; ++tile) {
-    load_tile(tile);
-    const float mt = xt.largest(), mq = xq.largest();
-    if (mt > x.rt + kLazy || mq > x.rq + kLazy) move_to<REVERSE>(x, fmaxf(x.rt, mt), fmaxf(x.rq, mq));
-    const uint64_t nt = pack2(-x.rt, -x.rt), nq = pack2(-x.rq, -x.rq);
-    uint64_t st = 0, sq = 0;
-    float t0 = 0.0f, t1 = 0.0f;
-#pragma unroll
-    for (int i = 0; i < TileT::kPairs; ++i) {
-      const uint64_t dt = add2(xt.pair(i), nt), dq = add2(xq.pair(i), nq);
-      float a0, a1, b0, b1, d0, d1;
-      unpack2(mul2(dt, scale), a0, a1);
-      unpack2(mul2(dq, scale), b0, b1);
-      a0 = ex2(a0);
-      a1 = ex2(a1);
-      b0 = ex2(b0);
-      b1 = ex2(b1);
-      st = add2(st, pack2(a0, a1));
-      sq = add2(sq, pack2(b0, b1));
-      unpack2(REVERSE ? fma2(dt, minus, dq) : fma2(dq, minus, dt), d0, d1);
-      // an entry without leading probability adds nothing (its difference may be
-      // infinite or NaN); one with it against a masked entry adds +inf
-      const float e0 = REVERSE ? b0 : a0, e1 = REVERSE ? b1 : a1;
-      if (e0 > 0.0f) t0 = __fmaf_rn(e0, d0, t0);
-      if (e1 > 0.0f) t1 = __fmaf_rn(e1, d1, t1);
+  if (warp == kNW) {  // ------------------------------------------- the issuing warp
+    bool fine = true;
+    auto issue = [&](int c, int m) {
+      const int b = c % kBuffers, k0 = lo + c * kChunk, k1 = min(hi, k0 + kChunk);
+      if (m > 0) fine = fine && mbar_wait(&sh.empty[b], (m - 1) & 1);
+      if (!fine || *(volatile int *)&sh.lost) return;
+      const int t0 = max(k0, rt.first), t1 = min(k1 + (rt.shift != 0), rt.last);
+      const int q0 = max(k0, rq.first), q1 = min(k1 + (rq.shift != 0), rq.last);
+      const uint32_t bt = t1 > t0 ? (t1 - t0) * 16 : 0, bq = q1 > q0 ? (q1 - q0) * 16 : 0;
+      mbar_arrive_expect_tx(&sh.full[b], bt + bq);
+      if (bt) tma_load_1d(buffer(c, 0) + (t0 - k0), rt.base + (int64_t)t0 * 16, bt, &sh.full[b]);
+      if (bq) tma_load_1d(buffer(c, 1) + (q0 - k0), rq.base + (int64_t)q0 * 16, bq, &sh.full[b]);
+    };
+    if (lane == 0)
+      for (int c = 0; c < n; ++c) issue(c, load_1(c));
+    __syncwarp();
+    if (S > 1) {
+      asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+      cluster.sync();
+    } else {
+      __syncthreads();
     }
-    float s0, s1;
-    unpack2(st, s0, s1);
-    x.st += s0 + s1;
-    unpack2(sq, s0, s1);
-    x.sq += s0 + s1;
-    x.t += t0 + t1;
+    if (out == nullptr || n <= kBuffers) return;
+    const Merged m = merge_parts<REVERSE>(sh.a, sh.t, S * kNW);
+    if (!m.empty && lane == 0)
+      for (int c = n - kBuffers - 1; c >= 0; --c) issue(c, load_2(c));
+    return;
   }
 
-  // --------------------------------- merge: the warp, then all warps of the cluster
-  auto merge_lanes = [&](PairSums &y) {
-    float Mt = y.rt, Mq = y.rq;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      Mt = fmaxf(Mt, __shfl_xor_sync(~0u, Mt, off));
-      Mq = fmaxf(Mq, __shfl_xor_sync(~0u, Mq, off));
+  // --------------------------------------------------------------- pass 1: the sums
+  ChunkTile<T, SHIFTED> xt, xq;
+  PairSums x;
+  // A copy that does not land in time (not expected) ends the copying and makes the
+  // results NaN; the copies still in flight, kBuffers at most, are waited for as well.
+  int lost = 0;
+  auto take = [&](int c, int m, bool wait) {
+    if (wait && lost <= kBuffers && (!mbar_wait(&sh.full[c % kBuffers], m & 1) || lost > 0)) {
+      ++lost;
+      *(volatile int *)&sh.lost = 1;
     }
-    move_to<REVERSE>(y, Mt, Mq);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      y.st += __shfl_xor_sync(~0u, y.st, off);
-      y.sq += __shfl_xor_sync(~0u, y.sq, off);
-      y.t += __shfl_xor_sync(~0u, y.t, off);
-    }
+    const int k0 = lo + c * kChunk;
+    xt.load(rt, grid, buffer(c, 0), k0, hi);
+    xq.load(rq, grid, buffer(c, 1), k0, hi);
   };
-  merge_lanes(x);
+  auto release = [&](int c) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.empty[c % kBuffers]);
+  };
+  for (int c = 0; c < n; ++c) {
+    take(c, load_1(c), true);
+    fold_pair<T, REVERSE>(x, xt, xq);
+    if (c + kBuffers < n) release(c);
+  }
+  if (lost > 0) x.st = quiet_nan();
+
+  // --------------------------------- merge: the warp, then all warps of the cluster
+  merge_lanes<REVERSE>(x);
   const float4 mine = make_float4(x.rt, x.st, x.rq, x.sq);
   if (S > 1) {
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA has begun
@@ -297,82 +442,38 @@ __global__ void __launch_bounds__(NT, 768 / NT) distill_kernel(DistillArgs a, in
     }
     __syncthreads();
   }
-  const int parts = S * kNW;
-  PairSums y;
-  for (int i = lane; i < parts; i += 32) {
-    const float4 p = sh.a[i];
-    y.rt = fmaxf(y.rt, p.x);
-    y.rq = fmaxf(y.rq, p.z);
-  }
-  for (int i = lane; i < parts; i += 32) {
-    const float4 p = sh.a[i];
-    PairSums z;
-    z.rt = p.x;
-    z.st = p.y;
-    z.rq = p.z;
-    z.sq = p.w;
-    z.t = sh.t[i];
-    move_to<REVERSE>(z, y.rt, y.rq);
-    y.st += z.st;
-    y.sq += z.sq;
-    y.t += z.t;
-  }
-  merge_lanes(y);
-
-  const bool bad = !(y.st < INFINITY) || !(y.sq < INFINITY);  // a NaN or +inf entry
-  const bool empty = !bad && (y.st == 0.0f || y.sq == 0.0f);  // a row masks every entry
-  const float lt = logf(y.st), lq = logf(y.sq);
-  float kl = REVERSE ? y.t / y.sq - lq + lt : y.t / y.st - lt + lq;
-  kl = bad ? quiet_nan() : kl < 0.0f ? 0.0f : kl;
-  if (rank == 0 && tid == 0) a.out_loss[r] = empty ? 0.0f : w * kl;
+  const Merged m = merge_parts<REVERSE>(sh.a, sh.t, S * kNW);
+  if (rank == 0 && tid == 0) a.out_loss[r] = m.empty ? 0.0f : w * m.kl;
   if (out == nullptr) return;
-  if (empty) {
+  if (m.empty) {
     zero_fill();
     return;
   }
 
-  // --------------------------------------------------------- pass 2: the gradient
-  const float wg = bad ? quiet_nan() : w;
-  const float c = kl == INFINITY ? quiet_nan() : lt - lq - kl;
-  const uint64_t mt2 = pack2(-y.rt, -y.rt), mq2 = pack2(-y.rq, -y.rq);
-  const uint64_t lt2 = pack2(-lt * kLog2e, -lt * kLog2e), lq2 = pack2(-lq * kLog2e, -lq * kLog2e);
-  const uint64_t w2 = pack2(wg, wg), c2 = pack2(c, c);
-  for (int tile = tiles - 1; tile >= 0; --tile) {
-    if (tile != tiles - 1) load_tile(tile);
-#pragma unroll
-    for (int i = 0; i < TileT::kPairs; ++i) {
-      const uint64_t dt = add2(xt.pair(i), mt2), dq = add2(xq.pair(i), mq2);
-      float q0, q1, g0, g1;
-      unpack2(fma2(dq, scale, lq2), q0, q1);
-      q0 = ex2(q0);
-      q1 = ex2(q1);
-      if (REVERSE) {
-        const uint64_t wq = mul2(w2, pack2(q0, q1));
-        unpack2(mul2(wq, add2(fma2(dt, minus, dq), c2)), g0, g1);
-        if (q0 == 0.0f) g0 = 0.0f;
-        if (q1 == 0.0f) g1 = 0.0f;
-        if (bad) g0 = g1 = quiet_nan();
-      } else {
-        float p0, p1;
-        unpack2(fma2(dt, scale, lt2), p0, p1);
-        unpack2(mul2(w2, fma2(pack2(ex2(p0), ex2(p1)), minus, pack2(q0, q1))), g0, g1);
-      }
-      xq.put(i, g0, g1);
+  // ----------------------------------------------------------- pass 2: the gradient
+  GradTerms g(m, w);
+  for (int c = n - 1; c >= 0; --c) {
+    take(c, load_2(c), c < n - kBuffers);
+    if (c >= kBuffers) release(c);
+    if (lost > 0) {
+      g.w = pack2(quiet_nan(), quiet_nan());
+      g.bad = true;
     }
-    const int base = lo + tile * kTile + tid;
+    gradient<T, REVERSE>(g, xt, xq);
 #pragma unroll
-    for (int j = 0; j < TileT::kAccesses; ++j) {
-      const int k = base + j * NT;
-      if (k < hi) xq.store(j, out + (int64_t)k * W);
+    for (int j = 0; j < kPackUnroll; ++j) {
+      const int k = lo + c * kChunk + j * kNT + tid;
+      if (k < hi) store_pack<T>(out, grid, k, xq.v[j]);
     }
   }
 }
 
-template <typename T, int W, int NT, bool REVERSE>
-cudaError_t launch(const DistillArgs &a, int S, cudaStream_t stream) {
+template <typename T, bool SHIFTED, bool REVERSE>
+cudaError_t launch_long(const DistillArgs &a, int S, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.B * a.K * S), 1, 1);
-  cfg.blockDim = dim3(NT, 1, 1);
+  cfg.blockDim = dim3(kNT + 32, 1, 1);
+  cfg.dynamicSmemBytes = kBuffers * 2 * kChunkBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -381,69 +482,72 @@ cudaError_t launch(const DistillArgs &a, int S, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = S > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, distill_kernel<T, W, NT, REVERSE>, a, S);
+  return cudaLaunchKernelEx(&cfg, distill_kernel<T, SHIFTED, REVERSE>, a, S);
 }
 
-constexpr int kSmallNT = 64, kNT = 256;
-
-template <typename T, int W, bool REVERSE>
+template <typename T, bool SHIFTED, bool REVERSE>
 cudaError_t plan(const DistillArgs &a, int S, cudaStream_t stream) {
-  // Short rows: one tile of 64 threads.
-  if (S == 0 && a.V <= Tile<T, W, kSmallNT>::kEntries * kSmallNT)
-    return launch<T, W, kSmallNT, REVERSE>(a, 1, stream);
-  // The fewest CTAs whose registers hold the pair of rows, 16 at most.
+  constexpr int kVW = Elem<T>::kPerVec;
+  // packs of a row, wherever it begins
+  const int64_t packs = ((int64_t)a.V + (SHIFTED ? 2 : 1) * (kVW - 1)) / kVW;
+  if (S == 0 && packs <= 2 * kSmallNT * kPackUnroll) {
+    distill_short_kernel<T, SHIFTED, REVERSE>
+        <<<(unsigned)(a.B * a.K), kSmallNT, 0, stream>>>(a);
+    return cudaGetLastError();
+  }
   if (S == 0) {
-    constexpr int64_t kTile = (int64_t)Tile<T, W, kNT>::kEntries * kNT;
-    const int64_t need = (a.V + kTile - 1) / kTile;
-    S = need < kMaxCluster ? (int)need : kMaxCluster;
+    const int64_t need = (packs + kBuffers * kChunk - 1) / (kBuffers * kChunk);
+    S = need < 8 ? (int)need : 8;
   }
   while (S > 1 && a.B * a.K * S > INT32_MAX) S /= 2;
-  return launch<T, W, kNT, REVERSE>(a, S, stream);
+  return launch_long<T, SHIFTED, REVERSE>(a, S, stream);
 }
 
-template <typename T, int W>
+template <typename T, bool SHIFTED>
 cudaError_t plan(const DistillArgs &a, int reverse, int S, cudaStream_t stream) {
-  return reverse ? plan<T, W, true>(a, S, stream) : plan<T, W, false>(a, S, stream);
+  return reverse ? plan<T, SHIFTED, true>(a, S, stream) : plan<T, SHIFTED, false>(a, S, stream);
 }
 
-template <typename T, int W>
-cudaError_t prepare() {
-  cudaError_t e = cudaFuncSetAttribute(distill_kernel<T, W, kNT, false>,
+template <typename T, bool SHIFTED, bool REVERSE>
+cudaError_t prepare_one() {
+  cudaError_t e = cudaFuncSetAttribute(distill_kernel<T, SHIFTED, REVERSE>,
                                        cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(distill_kernel<T, W, kNT, true>,
-                             cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    e = cudaFuncSetAttribute(distill_kernel<T, SHIFTED, REVERSE>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kBuffers * 2 * kChunkBytes);
+  return e;
+}
+template <typename T>
+cudaError_t prepare() {
+  cudaError_t e = prepare_one<T, false, false>();
+  if (e == cudaSuccess) e = prepare_one<T, false, true>();
+  if (e == cudaSuccess) e = prepare_one<T, true, false>();
+  if (e == cudaSuccess) e = prepare_one<T, true, true>();
   return e;
 }
 
 }  // namespace
 
 cudaError_t distill_prepare() {
-  cudaError_t e = prepare<float, 4>();
-  if (e == cudaSuccess) e = prepare<float, 1>();
-  if (e == cudaSuccess) e = prepare<uint16_t, 8>();
-  if (e == cudaSuccess) e = prepare<uint16_t, 2>();
-  if (e == cudaSuccess) e = prepare<uint16_t, 1>();
-  return e;
+  const cudaError_t e = prepare<float>();
+  return e == cudaSuccess ? prepare<uint16_t>() : e;
 }
 
 cudaError_t distill_launch(const DistillArgs &a, int dtype_bf16, int reverse, int S,
                            cudaStream_t stream) {
-  // The widest access that every row of all three arrays allows: their addresses,
-  // the strides and V in bytes are multiples of it.
-  const int elem = dtype_bf16 ? 2 : 4;
+  // Every row of all three arrays begins on a 16-byte boundary where their
+  // addresses, the strides and V in bytes are multiples of 16.
   const uint64_t bits =
       reinterpret_cast<uint64_t>(a.target) | reinterpret_cast<uint64_t>(a.draft) |
       reinterpret_cast<uint64_t>(a.out_grad) |
       (uint64_t)(a.target_stride_b | a.target_stride_k | a.draft_stride_b | a.draft_stride_k | a.V) *
-          elem;
-  if (dtype_bf16) {
-    if (bits % 16 == 0) return plan<uint16_t, 8>(a, reverse, S, stream);
-    return bits % 4 == 0 ? plan<uint16_t, 2>(a, reverse, S, stream)
-                         : plan<uint16_t, 1>(a, reverse, S, stream);
-  }
-  return bits % 16 == 0 ? plan<float, 4>(a, reverse, S, stream)
-                        : plan<float, 1>(a, reverse, S, stream);
+          (dtype_bf16 ? 2 : 4);
+  if (dtype_bf16)
+    return bits % 16 == 0 ? plan<uint16_t, false>(a, reverse, S, stream)
+                          : plan<uint16_t, true>(a, reverse, S, stream);
+  return bits % 16 == 0 ? plan<float, false>(a, reverse, S, stream)
+                        : plan<float, true>(a, reverse, S, stream);
 }
 
 }  // namespace specv

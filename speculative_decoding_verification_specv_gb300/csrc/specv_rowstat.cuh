@@ -199,4 +199,217 @@ __device__ __forceinline__ uint64_t warp_merge(uint64_t a, uint64_t b) {
   return a;
 }
 
+// ------------------------------------------------------ rows on another row's grid
+// A warp's share of a row, kU 16-byte packs per lane, on the grid of a row that
+// may sit differently against the 16-byte boundaries (the row of a contiguous
+// output, say, whose width no vector divides): pack k of the grid covers entries
+// [k VW - mis, (k + 1) VW - mis).  Lane l's j-th pack is k0 + 32 j + l.
+constexpr int kPackUnroll = 2;
+
+template <typename T>
+struct Grid {
+  int mis;      // entries before the row in its first pack
+  int V;
+  int count;    // packs
+  int full_lo, full_hi;  // packs wholly within the row
+
+  __device__ __forceinline__ Grid(const void *row, int V_) {
+    constexpr int VW = Elem<T>::kPerVec;
+    mis = (int)(reinterpret_cast<uint64_t>(row) % 16) / (int)sizeof(T);
+    V = V_;
+    count = (int)(((int64_t)V + mis + VW - 1) / VW);
+    full_lo = mis != 0 ? 1 : 0;
+    full_hi = (int)(((int64_t)V + mis) / VW);
+  }
+  __device__ __forceinline__ bool full(int k) const { return k >= full_lo && k < full_hi; }
+};
+
+// A row to be read on a grid.  Where its entries sit `shift` entries into the
+// aligned vectors of memory, a pack is joined from two of them, the second of
+// which is the next lane's first: one load per pack and lane, and shuffles.
+template <typename T, bool SHIFTED>
+struct GridRow {
+  const T *row;
+  const char *base;   // the vector that holds the grid's pack 0 (or its start)
+  int shift;          // 0..VW-1
+  int lo, hi;         // packs whose vectors lie within the row
+  int first, last;    // the row's whole vectors, counted from base
+
+  __device__ __forceinline__ GridRow(const T *row_, const Grid<T> &grid) {
+    constexpr int VW = Elem<T>::kPerVec;
+    row = row_;
+    const uint64_t at = reinterpret_cast<uint64_t>(row);
+    if (!SHIFTED) {
+      base = reinterpret_cast<const char *>(at);
+      shift = 0;
+      lo = first = 0;
+      hi = last = grid.full_hi;
+      return;
+    }
+    const int mis = (int)(at % 16) / (int)sizeof(T);
+    const int d = mis - grid.mis;  // where the grid's pack 0 begins in the row's own vectors
+    const int back = d < 0 ? 1 : 0;
+    shift = d + back * VW;
+    base = reinterpret_cast<const char *>(at - at % 16) - back * 16;
+    // pack k is joined from vectors k - back and, with a shift, k - back + 1
+    lo = first = back + (mis != 0 ? 1 : 0);
+    last = (int)(((int64_t)grid.V + mis) / VW) + back;
+    hi = last - (shift != 0 ? 1 : 0);
+  }
+};
+
+// VW entries from `shift` (1..VW-1) entries into vector a, continued in vector b.
+template <typename T>
+__device__ __forceinline__ uint4 shifted(const uint4 &a, const uint4 &b, int shift) {
+  const int words = sizeof(T) == 2 ? shift >> 1 : shift;
+  uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if (words & 2) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) x[i] = x[i + 2];
+  }
+  if (words & 1) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) x[i] = x[i + 1];
+  }
+  if (sizeof(T) == 2 && (shift & 1)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = __funnelshift_r(x[i], x[i + 1], 16);
+  }
+  return make_uint4(x[0], x[1], x[2], x[3]);
+}
+
+// Puts entries 2 i and 2 i + 1 of a vector, rounded to the logits' type.
+template <typename T>
+__device__ __forceinline__ void put_pair(uint4 &x, int i, float a, float b) {
+  if constexpr (sizeof(T) == 2) {
+    uint32_t &w = i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
+  } else if (i == 0) {
+    x.x = __float_as_uint(a);
+    x.y = __float_as_uint(b);
+  } else {
+    x.z = __float_as_uint(a);
+    x.w = __float_as_uint(b);
+  }
+}
+
+template <typename T, bool SHIFTED>
+struct PackTile {
+  uint4 v[kPackUnroll + (SHIFTED ? 1 : 0)];
+  bool joined;  // the packs are whole (else v holds vectors still to be joined)
+
+  __device__ __forceinline__ static uint4 load16(const char *p) {
+    uint4 x;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                 : "l"(p));
+    return x;
+  }
+  __device__ __forceinline__ static uint4 none() {
+    constexpr uint32_t n = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+    return make_uint4(n, n, n, n);
+  }
+  // pack k entry by entry: what lies outside the row is -inf
+  __device__ __noinline__ static uint4 load_entries(const T *row, int64_t first, int V) {
+    uint4 x = none();
+#pragma unroll
+    for (int e = 0; e < Elem<T>::kPerVec; ++e) {
+      const int64_t c = first + e;
+      if (c >= 0 && c < V) {
+        uint32_t bits;
+        if constexpr (sizeof(T) == 2) {
+          uint16_t h;
+          asm volatile("ld.global.u16 %0, [%1];" : "=h"(h) : "l"(row + c));
+          bits = h;
+        } else {
+          asm volatile("ld.global.u32 %0, [%1];" : "=r"(bits) : "l"(row + c));
+        }
+        Elem<T>::put_bits(x, e, bits);
+      }
+    }
+    return x;
+  }
+
+  // The packs k0 + 32 j + lane below `end`; the others are -inf.
+  __device__ __forceinline__ void load(const GridRow<T, SHIFTED> &r, const Grid<T> &grid, int k0,
+                                       int end) {
+    constexpr int VW = Elem<T>::kPerVec;
+    const int lane = threadIdx.x & 31;
+    if (k0 >= r.lo && k0 + 32 * kPackUnroll <= min(r.hi, end)) {
+      const char *p = r.base + ((int64_t)k0 + lane) * 16;
+#pragma unroll
+      for (int j = 0; j < kPackUnroll; ++j) v[j] = load16(p + j * 512);
+      if (SHIFTED) {
+        joined = r.shift == 0;
+        // lane 31's second vector of the last pack, fetched by lane 0
+        if (!joined && lane == 0) v[kPackUnroll] = load16(p + kPackUnroll * 512);
+      }
+      return;
+    }
+    joined = true;
+#pragma unroll
+    for (int j = 0; j < kPackUnroll; ++j) {
+      const int k = k0 + 32 * j + lane;
+      v[j] = none();
+      if (k < end) {
+        if (k >= r.lo && k < r.hi && r.shift == 0)
+          v[j] = load16(r.base + (int64_t)k * 16);
+        else
+          v[j] = load_entries(r.row, (int64_t)k * VW - grid.mis, grid.V);
+      }
+    }
+  }
+
+  // Joins the packs from their vectors (every lane of the warp).
+  __device__ __forceinline__ void join(const GridRow<T, SHIFTED> &r) {
+    if (!SHIFTED || joined) return;
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < kPackUnroll; ++j) {
+      const uint4 &n = v[j + 1];
+      uint4 next;  // the next lane's vector; lane 31's is the next pack's first
+      next.x = __shfl_sync(0xffffffffu, lane == 0 ? n.x : v[j].x, (lane + 1) & 31);
+      next.y = __shfl_sync(0xffffffffu, lane == 0 ? n.y : v[j].y, (lane + 1) & 31);
+      next.z = __shfl_sync(0xffffffffu, lane == 0 ? n.z : v[j].z, (lane + 1) & 31);
+      next.w = __shfl_sync(0xffffffffu, lane == 0 ? n.w : v[j].w, (lane + 1) & 31);
+      v[j] = shifted<T>(v[j], next, r.shift);
+    }
+    joined = true;
+  }
+
+  __device__ __forceinline__ uint64_t pair(int i) const {
+    constexpr int kEach = Elem<T>::kPerVec / 2;
+    return pair_of<T>(v[i / kEach], i % kEach);
+  }
+  __device__ __forceinline__ float largest() const {
+    float m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < kPackUnroll; ++j) m = fmaxf(m, vector_max<T>(v[j]));
+    return m;
+  }
+  __device__ __forceinline__ void put(int i, float a, float b) {
+    constexpr int kEach = Elem<T>::kPerVec / 2;
+    put_pair<T>(v[i / kEach], i % kEach, a, b);
+  }
+};
+template <typename T>
+constexpr int kTilePairs = kPackUnroll * Elem<T>::kPerVec / 2;  // packed pairs of a PackTile
+
+// Writes a pack of a row on its own grid: a full one as one access, an edge one
+// entry by entry.
+template <typename T>
+__device__ __forceinline__ void store_pack(T *row, const Grid<T> &grid, int k, const uint4 &v) {
+  constexpr int VW = Elem<T>::kPerVec;
+  T *p = row + ((int64_t)k * VW - grid.mis);
+  if (grid.full(k)) {
+    *reinterpret_cast<uint4 *>(p) = v;
+  } else {
+#pragma unroll
+    for (int e = 0; e < VW; ++e) {
+      const int64_t c = (int64_t)k * VW - grid.mis + e;
+      if (c >= 0 && c < grid.V) p[e] = narrow<T>(Elem<T>::get(v, e));
+    }
+  }
+}
+
 }  // namespace specv
