@@ -62,13 +62,7 @@ struct Merged {
 
 template <bool REVERSE>
 __device__ __forceinline__ void merge_lanes(PairSums &y) {
-  float Mt = y.rt, Mq = y.rq;
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    Mt = fmaxf(Mt, __shfl_xor_sync(~0u, Mt, off));
-    Mq = fmaxf(Mq, __shfl_xor_sync(~0u, Mq, off));
-  }
-  move_to<REVERSE>(y, Mt, Mq);
+  move_to<REVERSE>(y, warp_max(y.rt), warp_max(y.rq));
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
     y.st += __shfl_xor_sync(~0u, y.st, off);
@@ -112,6 +106,13 @@ __device__ __forceinline__ Merged merge_parts(const float4 *a, const float *t, i
   return m;
 }
 
+// t += e d where e > 0, else nothing, whatever d is.
+__device__ __forceinline__ void fma_if_positive(float &t, float e, float d) {
+  asm("{\n\t.reg .pred p;\n\tsetp.gt.f32 p, %1, 0f00000000;\n\t@p fma.rn.f32 %0, %1, %2, %0;\n\t}"
+      : "+f"(t)
+      : "f"(e), "f"(d));
+}
+
 // Adds the entries of two tiles to the sums.
 template <typename T, bool REVERSE, typename TileT>
 __device__ __forceinline__ void fold_pair(PairSums &x, const TileT &xt, const TileT &xq) {
@@ -123,7 +124,7 @@ __device__ __forceinline__ void fold_pair(PairSums &x, const TileT &xt, const Ti
   uint64_t st = 0, sq = 0;
   float t0 = 0.0f, t1 = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kTilePairs<T>; ++i) {
+  for (int i = 0; i < TileT::kPairs; ++i) {
     const uint64_t dt = add2(xt.pair(i), nt), dq = add2(xq.pair(i), nq);
     float a0, a1, b0, b1, d0, d1;
     unpack2(mul2(dt, scale), a0, a1);
@@ -138,8 +139,8 @@ __device__ __forceinline__ void fold_pair(PairSums &x, const TileT &xt, const Ti
     // an entry without leading probability adds nothing (its difference may be
     // infinite or NaN); one with it against a masked entry adds +inf
     const float e0 = REVERSE ? b0 : a0, e1 = REVERSE ? b1 : a1;
-    if (e0 > 0.0f) t0 = __fmaf_rn(e0, d0, t0);
-    if (e1 > 0.0f) t1 = __fmaf_rn(e1, d1, t1);
+    fma_if_positive(t0, e0, d0);
+    fma_if_positive(t1, e1, d1);
   }
   float s0, s1;
   unpack2(st, s0, s1);
@@ -173,7 +174,7 @@ template <typename T, bool REVERSE, typename TileT>
 __device__ __forceinline__ void gradient(const GradTerms &g, const TileT &xt, TileT &xq) {
   const uint64_t scale = pack2(kLog2e, kLog2e), minus = pack2(-1.0f, -1.0f);
 #pragma unroll
-  for (int i = 0; i < kTilePairs<T>; ++i) {
+  for (int i = 0; i < TileT::kPairs; ++i) {
     const uint64_t dt = add2(xt.pair(i), g.rt), dq = add2(xq.pair(i), g.rq);
     float q0, q1, g0, g1;
     unpack2(fma2(dq, scale, g.lq), q0, q1);
@@ -262,10 +263,11 @@ __global__ void __launch_bounds__(kSmallNT) distill_short_kernel(DistillArgs a) 
 }
 
 // -------------------------------------------------------------------- long rows
-constexpr int kNT = 256;            // consuming threads; one more warp issues the copies
-constexpr int kChunk = kNT * kPackUnroll;          // packs of a chunk
+constexpr int kNT = 128;     // consuming threads; one more warp issues the copies
+constexpr int kUnroll = 2;   // packs per thread of a chunk
+constexpr int kChunk = kNT * kUnroll;              // packs of a chunk
 constexpr int kChunkBytes = (kChunk + 1) * 16;     // a shifted row's chunk needs one vector more
-constexpr int kBuffers = 4;                        // chunks of both rows held per CTA
+constexpr int kBuffers = 6;                        // chunks of both rows held per CTA
 
 struct __align__(16) DistillShared {
   float4 a[kMaxCluster * (kNT / 32)];  // (rt, st, rq, sq) of every warp of the cluster
@@ -274,24 +276,35 @@ struct __align__(16) DistillShared {
   int lost;  // set when a copy did not land in time
 };
 
-// A thread's packs of a chunk, read from shared memory (edge packs from the row).
+// A thread's packs of a chunk, read from shared memory.  Edge packs are read from the
+// row; `inner`: the chunk has none, and no end.
 template <typename T, bool SHIFTED>
 struct ChunkTile {
-  uint4 v[kPackUnroll];
+  static constexpr int kPairs = kUnroll * Elem<T>::kPerVec / 2;
+  uint4 v[kUnroll];
   __device__ __forceinline__ void load(const GridRow<T, SHIFTED> &r, const Grid<T> &grid,
-                                       const uint4 *buf, int k0, int end) {
+                                       const uint4 *buf, int k0, int end, bool inner) {
     constexpr int VW = Elem<T>::kPerVec;
+    const uint4 *p = buf + (int)threadIdx.x;
+    if (inner) {
 #pragma unroll
-    for (int j = 0; j < kPackUnroll; ++j) {
-      const int i = j * kNT + (int)threadIdx.x, k = k0 + i;
-      if (!SHIFTED) {
-        v[j] = k < end ? buf[i] : PackTile<T, false>::none();
-      } else if (k >= r.lo && k < min(r.hi, end)) {
-        v[j] = buf[i];
-        if (r.shift != 0) v[j] = shifted<T>(v[j], buf[i + 1], r.shift);
-      } else {
-        v[j] = PackTile<T, true>::none();
-        if (k < end) v[j] = PackTile<T, true>::load_entries(r.row, (int64_t)k * VW - grid.mis, grid.V);
+      for (int j = 0; j < kUnroll; ++j) v[j] = p[j * kNT];
+      if (SHIFTED && r.shift != 0) {
+#pragma unroll
+        for (int j = 0; j < kUnroll; ++j) v[j] = shifted<T>(v[j], p[j * kNT + 1], r.shift);
+      }
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j) {
+      const int k = k0 + j * kNT + (int)threadIdx.x;
+      v[j] = PackTile<T, SHIFTED>::none();
+      if (k >= end) continue;
+      if (k >= r.lo && k < r.hi) {
+        v[j] = p[j * kNT];
+        if (SHIFTED && r.shift != 0) v[j] = shifted<T>(v[j], p[j * kNT + 1], r.shift);
+      } else if (SHIFTED) {
+        v[j] = PackTile<T, SHIFTED>::load_entries(r.row, (int64_t)k * VW - grid.mis, grid.V);
       }
     }
   }
@@ -302,7 +315,7 @@ struct ChunkTile {
   __device__ __forceinline__ float largest() const {
     float m = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < kPackUnroll; ++j) m = fmaxf(m, vector_max<T>(v[j]));
+    for (int j = 0; j < kUnroll; ++j) m = fmaxf(m, vector_max<T>(v[j]));
     return m;
   }
   __device__ __forceinline__ void put(int i, float a, float b) {
@@ -311,12 +324,34 @@ struct ChunkTile {
   }
 };
 
+// Waits as mbar_wait does, for phase `parity` of `bar`, at most kWaitLimitNs; the
+// thread is suspended meanwhile (kSuspendNs at a time) instead of polling: warps that
+// poll take the issue slots of those at work.
+constexpr uint32_t kSuspendNs = 1000 * 1000;
+__device__ __forceinline__ bool wait_suspended(uint64_t *bar, uint32_t parity) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 0; it < kSpinLimit; ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendNs)
+        : "memory");
+    if (ok) return true;
+    if (it == 0) t0 = global_timer_ns();
+    if (global_timer_ns() - t0 > kWaitLimitNs) break;
+  }
+  return false;
+}
+
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 template <typename T, bool SHIFTED, bool REVERSE>
-__global__ void __launch_bounds__(kNT + 32, 3) distill_kernel(DistillArgs a, int S) {
+__global__ void __launch_bounds__(kNT + 32, 4) distill_kernel(DistillArgs a, int S) {
   constexpr int kNW = kNT / 32;
   extern __shared__ __align__(16) unsigned char chunks[];  // [kBuffers][2][kChunkBytes]
   __shared__ DistillShared sh;
@@ -374,7 +409,7 @@ __global__ void __launch_bounds__(kNT + 32, 3) distill_kernel(DistillArgs a, int
     bool fine = true;
     auto issue = [&](int c, int m) {
       const int b = c % kBuffers, k0 = lo + c * kChunk, k1 = min(hi, k0 + kChunk);
-      if (m > 0) fine = fine && mbar_wait(&sh.empty[b], (m - 1) & 1);
+      if (m > 0) fine = fine && wait_suspended(&sh.empty[b], (m - 1) & 1);
       if (!fine || *(volatile int *)&sh.lost) return;
       const int t0 = max(k0, rt.first), t1 = min(k1 + (rt.shift != 0), rt.last);
       const int q0 = max(k0, rq.first), q1 = min(k1 + (rq.shift != 0), rq.last);
@@ -405,21 +440,28 @@ __global__ void __launch_bounds__(kNT + 32, 3) distill_kernel(DistillArgs a, int
   // A copy that does not land in time (not expected) ends the copying and makes the
   // results NaN; the copies still in flight, kBuffers at most, are waited for as well.
   int lost = 0;
-  auto take = [&](int c, int m, bool wait) {
-    if (wait && lost <= kBuffers && (!mbar_wait(&sh.full[c % kBuffers], m & 1) || lost > 0)) {
+  // packs that are whole in all three rows
+  const int in_lo = max(max(rt.lo, rq.lo), grid.full_lo);
+  const int in_hi = min(min(rt.hi, rq.hi), min(grid.full_hi, hi));
+  auto is_inner = [&](int c) {
+    const int k0 = lo + c * kChunk;
+    return k0 >= in_lo && k0 + kChunk <= in_hi;
+  };
+  auto take = [&](int c, int m, bool wait, bool inner) {
+    if (wait && lost <= kBuffers && (!wait_suspended(&sh.full[c % kBuffers], m & 1) || lost > 0)) {
       ++lost;
       *(volatile int *)&sh.lost = 1;
     }
     const int k0 = lo + c * kChunk;
-    xt.load(rt, grid, buffer(c, 0), k0, hi);
-    xq.load(rq, grid, buffer(c, 1), k0, hi);
+    xt.load(rt, grid, buffer(c, 0), k0, hi, inner);
+    xq.load(rq, grid, buffer(c, 1), k0, hi, inner);
   };
   auto release = [&](int c) {
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.empty[c % kBuffers]);
   };
   for (int c = 0; c < n; ++c) {
-    take(c, load_1(c), true);
+    take(c, load_1(c), true, is_inner(c));
     fold_pair<T, REVERSE>(x, xt, xq);
     if (c + kBuffers < n) release(c);
   }
@@ -453,17 +495,23 @@ __global__ void __launch_bounds__(kNT + 32, 3) distill_kernel(DistillArgs a, int
   // ----------------------------------------------------------- pass 2: the gradient
   GradTerms g(m, w);
   for (int c = n - 1; c >= 0; --c) {
-    take(c, load_2(c), c < n - kBuffers);
+    const bool inner = is_inner(c);
+    take(c, load_2(c), c < n - kBuffers, inner);
     if (c >= kBuffers) release(c);
     if (lost > 0) {
       g.w = pack2(quiet_nan(), quiet_nan());
       g.bad = true;
     }
     gradient<T, REVERSE>(g, xt, xq);
+    const int k0 = lo + c * kChunk + tid;
+    if (inner) {
+      uint4 *to = reinterpret_cast<uint4 *>(out + ((int64_t)k0 * Elem<T>::kPerVec - grid.mis));
 #pragma unroll
-    for (int j = 0; j < kPackUnroll; ++j) {
-      const int k = lo + c * kChunk + j * kNT + tid;
-      if (k < hi) store_pack<T>(out, grid, k, xq.v[j]);
+      for (int j = 0; j < kUnroll; ++j) to[j * kNT] = xq.v[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j)
+        if (k0 + j * kNT < hi) store_pack<T>(out, grid, k0 + j * kNT, xq.v[j]);
     }
   }
 }

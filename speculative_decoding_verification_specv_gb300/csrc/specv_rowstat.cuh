@@ -19,10 +19,18 @@ namespace specv {
 // (which is 0 there): a masked entry then adds 0 * kFarBelow and not 0 * -inf.
 constexpr float kFarBelow = -1e4f;
 
-// Where row r = (b, n) of a [B][N][V] view with element strides (sb, sn, 1) begins.
+// Where row r = (b, n) of a [B][N][V] view with element strides (sb, sn, 1) begins
+// (B * N < 2^31).
 __device__ __forceinline__ int64_t row_offset(int64_t r, int N, int64_t sb, int64_t sn) {
-  const int64_t b = r / N;
-  return b * sb + (r - b * N) * sn;
+  const uint32_t b = (uint32_t)r / (uint32_t)N, n = (uint32_t)r - b * (uint32_t)N;
+  return b * sb + n * sn;
+}
+
+// Maximum over the warp; a NaN is passed over.
+__device__ __forceinline__ float warp_max(float x) {
+  float m;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+  return m;
 }
 
 __device__ __forceinline__ float quiet_nan() { return __int_as_float(0x7fffffff); }
@@ -295,6 +303,7 @@ __device__ __forceinline__ void put_pair(uint4 &x, int i, float a, float b) {
 
 template <typename T, bool SHIFTED>
 struct PackTile {
+  static constexpr int kPairs = kPackUnroll * Elem<T>::kPerVec / 2;  // packed pairs of entries
   uint4 v[kPackUnroll + (SHIFTED ? 1 : 0)];
   bool joined;  // the packs are whole (else v holds vectors still to be joined)
 
@@ -392,9 +401,6 @@ struct PackTile {
     put_pair<T>(v[i / kEach], i % kEach, a, b);
   }
 };
-template <typename T>
-constexpr int kTilePairs = kPackUnroll * Elem<T>::kPerVec / 2;  // packed pairs of a PackTile
-
 // Writes a pack of a row on its own grid: a full one as one access, an edge one
 // entry by entry.
 template <typename T>
