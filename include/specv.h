@@ -547,7 +547,7 @@ typedef struct {
     const void *grad; /* device pointer, aligned to its element */
     void *out;        /* where the clipped values go: `grad` itself, or memory that
                        * overlaps no gradient */
-    int64_t count;    /* >= 0 */
+    int64_t count;    /* >= 0; at most 2^40 over all gradients */
     int64_t dtype;    /* a specv_dtype */
 } specv_grad;
 

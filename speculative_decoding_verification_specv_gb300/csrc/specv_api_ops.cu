@@ -26,6 +26,7 @@ specv_status status_of(cudaError_t e) {
 }
 
 constexpr int64_t kLimit = (int64_t)1 << 62;
+constexpr int64_t kClipElements = (int64_t)1 << 40;  // chunk numbers stay below 2^31
 
 // Sizes and strides of a [B][N][V] view: every element offset stays below 2^62.
 bool view_ok(int64_t B, int32_t N, int32_t V, int64_t sb, int64_t sn) {
@@ -147,14 +148,16 @@ specv_status specv_clip_grads(const specv_grad *grads, int64_t n, float max_norm
                               void *stream) {
   NvtxRange range("specv_clip_grads");
   if (n < 0 || (n > 0 && !grads) || !out_norm || !(max_norm >= 0.0f)) return SPECV_ERR_INVALID_ARG;
-  int64_t live = 0;  // gradients with elements
+  int64_t live = 0, elements = 0;  // gradients with elements, and those
   for (int64_t i = 0; i < n; ++i) {
     const specv_grad &g = grads[i];
-    if (g.count < 0 || g.count > kLimit / 4 || !dtype_ok(g.dtype)) return SPECV_ERR_INVALID_ARG;
+    if (g.count < 0 || g.count > kClipElements || !dtype_ok(g.dtype)) return SPECV_ERR_INVALID_ARG;
     if (g.count == 0) continue;
     if (!g.grad || !g.out || misaligned(g.grad, g.dtype) || misaligned(g.out, g.dtype))
       return SPECV_ERR_INVALID_ARG;
     ++live;
+    elements += g.count;
+    if (elements > kClipElements) return SPECV_ERR_INVALID_ARG;
   }
   int sms = 0;
   const int ready = specv::device_ready(&sms);
@@ -189,14 +192,16 @@ specv_status specv_clip_grads(const specv_grad *grads, int64_t n, float max_norm
     for (int64_t g = 0; g < groups && e == cudaSuccess; ++g) {
       a.n = 0;
       a.chunks = 0;
+      a.in_place = 1;
       for (; at < n && a.n < specv::kClipTensors; ++at) {
         if (grads[at].count == 0) continue;
         const int k = a.n++;
+        a.in_place &= grads[at].out == grads[at].grad;
         a.in[k] = grads[at].grad;
         a.out[k] = grads[at].out;
         a.count[k] = grads[at].count;
         a.bf16[k] = grads[at].dtype == SPECV_BF16;
-        a.first[k] = a.chunks;
+        a.first[k] = (int)a.chunks;
         a.chunks += specv::clip_chunks(a.in[k], a.count[k], a.bf16[k]);
       }
       int grid = a.chunks < per_launch ? (int)a.chunks : per_launch;
@@ -208,7 +213,7 @@ specv_status specv_clip_grads(const specv_grad *grads, int64_t n, float max_norm
         a.partials = partials;
         e = specv::clip_norm_launch(a, grid, st);
       } else {
-        e = specv::clip_scale_launch(a, grid, st);
+        e = specv::clip_scale_launch(a, grid, g == 0, st);
       }
     }
   }

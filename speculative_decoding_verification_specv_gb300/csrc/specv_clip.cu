@@ -3,11 +3,17 @@
 //
 //   norm = sqrt(sum_tensors sum_i x_i^2),  c = min(1, max_norm / (norm + eps)),
 //   out_i = round(c x_i)
-// Two launches.  The first sums squares: chunk k of kChunkBytes (whole tensors
-// are cut into chunks, tensor by tensor) goes to CTA k mod grid, each thread
-// adds at most kChunkBytes / (4 NT) squares in fp32 and then the chunk to a
-// double.  The CTAs' sums are written out; every CTA of the second launch adds
-// them in the same order, so all hold the same norm, and scales its chunks.
+// Two launches.  Each gradient is cut into chunks of kChunkBytes of the aligned
+// memory that holds it (the first may begin before the gradient, off a 16-byte
+// boundary, the last end after it; what is not the gradient's is not read), and
+// the chunks of all gradients are dealt to the CTAs in turn.  The first launch
+// sums squares, in fp32 within a thread's share of a chunk (two interleaved sums of
+// up to 32 terms) and in fp64 beyond; every CTA writes its sum.  Every CTA of the
+// second launch adds those sums in the same order, so that all hold the same norm
+// (no atomics, one result), and scales its chunks, the last ones first: these the
+// first launch has left in L2.  The second launch begins while the first drains
+// (programmatic dependent launch).  Gradients of a call travel in the launches'
+// parameters, so nothing is copied to the device first.
 #include "specv_internal.h"
 #include "specv_rowstat.cuh"
 
@@ -16,87 +22,196 @@ namespace specv {
 namespace {
 
 constexpr int kNT = 256;
-constexpr int kChunk = 8192;  // elements
+constexpr int kVecs = 8;                              // 16-byte vectors per thread and chunk
+constexpr int kChunkBytes = kNT * kVecs * 16;
 
-__device__ __forceinline__ int find_tensor(const ClipArgs &a, int64_t chunk) {
-  int lo = 0, hi = a.n - 1;  // the last tensor that begins at or before the chunk
+// The gradient that chunk k belongs to.
+__device__ __forceinline__ int find_tensor(const ClipArgs &a, int k) {
+  int lo = 0, hi = a.n - 1;  // the last one that begins at or before the chunk
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (a.first[mid] <= chunk) lo = mid;
+    if (a.first[mid] <= k) lo = mid;
     else hi = mid - 1;
   }
   return lo;
 }
 
-__device__ __forceinline__ float load_any(const ClipArgs &a, int t, int64_t i) {
-  return a.bf16[t] ? bf16_bits_to_float(static_cast<const uint16_t *>(a.in[t])[i])
-                   : static_cast<const float *>(a.in[t])[i];
+__device__ __forceinline__ uint4 load16(const char *p) {
+  uint4 x;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+               : "l"(p));
+  return x;
+}
+
+// A chunk: its vectors lie at base + 16 (tid + u kNT); entry e of that vector is entry
+// at + (tid + u kNT) VW + e of the gradient, which has `count` entries.
+struct Chunk {
+  const char *base;
+  int64_t at, count;
+  bool whole;  // every vector lies within the gradient
+};
+__device__ __forceinline__ Chunk chunk_of(const ClipArgs &a, int t, int k, int elem) {
+  const uint64_t p = reinterpret_cast<uint64_t>(a.in[t]);
+  const int mis = (int)(p % 16) / elem, per_vec = 16 / elem;
+  Chunk c;
+  const int64_t vec = (int64_t)(k - a.first[t]) * (kNT * kVecs);
+  c.base = reinterpret_cast<const char *>(p - p % 16) + vec * 16;
+  c.at = vec * per_vec - mis;
+  c.count = a.count[t];
+  c.whole = c.at >= 0 && c.at + (int64_t)kNT * kVecs * per_vec <= c.count;
+  return c;
+}
+
+// Sum of the squares of a vector's entries, in two interleaved sums.
+template <typename T>
+__device__ __forceinline__ uint64_t add_squares(uint64_t s, const uint4 &v) {
+#pragma unroll
+  for (int i = 0; i < Elem<T>::kPerVec / 2; ++i) {
+    const uint64_t x = pair_of<T>(v, i);
+    s = fma2(x, x, s);
+  }
+  return s;
+}
+
+template <typename T>
+__device__ __forceinline__ float chunk_squares(const Chunk &c) {
+  constexpr int VW = Elem<T>::kPerVec;
+  uint4 v[kVecs];
+  if (c.whole) {
+    const char *p = c.base + (int)threadIdx.x * 16;
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) v[u] = load16(p + u * (kNT * 16));
+  } else {
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+      const int i = (int)threadIdx.x + u * kNT;
+      const int64_t first = c.at + (int64_t)i * VW;
+      v[u] = make_uint4(0, 0, 0, 0);
+      if (first >= 0 && first + VW <= c.count) {
+        v[u] = load16(c.base + (int64_t)i * 16);
+      } else if (first < c.count && first + VW > 0) {
+        const T *p = reinterpret_cast<const T *>(c.base + (int64_t)i * 16);
+#pragma unroll
+        for (int e = 0; e < VW; ++e)
+          if (first + e >= 0 && first + e < c.count) Elem<T>::put_bits(v[u], e, Elem<T>::load_bits(p + e));
+      }
+    }
+  }
+  uint64_t s = 0;
+#pragma unroll
+  for (int u = 0; u < kVecs; ++u) s = add_squares<T>(s, v[u]);
+  float s0, s1;
+  unpack2(s, s0, s1);
+  return s0 + s1;
 }
 
 __device__ __forceinline__ double block_sum_d(double *red, double x) {
+#pragma unroll
   for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(~0u, x, off);
-  __syncthreads();
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
   __syncthreads();
   x = 0.0;
+#pragma unroll
   for (int w = 0; w < kNT / 32; ++w) x += red[w];
   return x;
 }
 
-__global__ void __launch_bounds__(kNT) clip_norm_kernel(const __grid_constant__ ClipArgs a) {
+__global__ void __launch_bounds__(kNT, 4) clip_norm_kernel(const __grid_constant__ ClipArgs a) {
   __shared__ double red[kNT / 32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   double sum = 0.0;
   for (int64_t k = blockIdx.x; k < a.chunks; k += gridDim.x) {
-    const int t = find_tensor(a, k);
-    const int64_t lo = (k - a.first[t]) * kChunk, hi = min(a.count[t], lo + kChunk);
-    float s = 0.0f;
-    for (int64_t i = lo + threadIdx.x; i < hi; i += kNT) {
-      const float x = load_any(a, t, i);
-      s = __fmaf_rn(x, x, s);
-    }
-    sum += (double)s;
+    const int t = find_tensor(a, (int)k);
+    sum += (double)(a.bf16[t] ? chunk_squares<uint16_t>(chunk_of(a, t, (int)k, 2))
+                              : chunk_squares<float>(chunk_of(a, t, (int)k, 4)));
   }
   sum = block_sum_d(red, sum);
   if (threadIdx.x == 0) a.partial[a.partial_at + blockIdx.x] = sum;
 }
 
-__global__ void __launch_bounds__(kNT) clip_scale_kernel(const __grid_constant__ ClipArgs a) {
+// A vector's entries times c, rounded once.
+template <typename T>
+__device__ __forceinline__ uint4 scaled(const uint4 &v, uint64_t c) {
+  uint4 y;
+#pragma unroll
+  for (int i = 0; i < Elem<T>::kPerVec / 2; ++i) {
+    float a, b;
+    unpack2(mul2(pair_of<T>(v, i), c), a, b);
+    put_pair<T>(y, i, a, b);
+  }
+  return y;
+}
+
+template <typename T>
+__device__ __forceinline__ void scale_chunk(const ClipArgs &a, int t, const Chunk &c, float factor) {
+  constexpr int VW = Elem<T>::kPerVec;
+  const T *in = static_cast<const T *>(a.in[t]);
+  T *out = static_cast<T *>(a.out[t]);
+  const uint64_t f = pack2(factor, factor);
+  // vectors where the output lies as the input against the 16-byte boundaries
+  const bool alike = (reinterpret_cast<uint64_t>(in) - reinterpret_cast<uint64_t>(out)) % 16 == 0;
+  if (alike && c.whole) {
+    uint4 v[kVecs];
+    const char *p = c.base + (int)threadIdx.x * 16;
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) v[u] = load16(p + u * (kNT * 16));
+    uint4 *q = reinterpret_cast<uint4 *>(out + c.at) + threadIdx.x;
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) q[u * kNT] = scaled<T>(v[u], f);
+    return;
+  }
+  const int64_t lo = c.at < 0 ? 0 : c.at, end = c.at + (int64_t)kNT * kVecs * VW;
+  const int64_t hi = end < c.count ? end : c.count;
+#pragma unroll 4
+  for (int64_t i = lo + threadIdx.x; i < hi; i += kNT)
+    out[i] = narrow<T>(__fmul_rn(factor, widen(in[i])));
+}
+
+__global__ void __launch_bounds__(kNT, 4) clip_scale_kernel(const __grid_constant__ ClipArgs a) {
   __shared__ double red[kNT / 32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   double sum = 0.0;
   for (int i = threadIdx.x; i < a.partials; i += kNT) sum += a.partial[i];
   const float norm = (float)sqrt(block_sum_d(red, sum));
   if (a.out_norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *a.out_norm = norm;
   // a norm that is not finite gives no factor: the values are left as they are
   const float c = norm < INFINITY ? fminf(1.0f, a.max_norm / (norm + kClipEps)) : 1.0f;
-  for (int64_t k = blockIdx.x; k < a.chunks; k += gridDim.x) {
-    const int t = find_tensor(a, k);
+  if (c == 1.0f && a.in_place) return;
+  for (int64_t j = a.chunks - 1 - blockIdx.x; j >= 0; j -= gridDim.x) {
+    const int k = (int)j, t = find_tensor(a, k);
     if (c == 1.0f && a.out[t] == a.in[t]) continue;
-    const int64_t lo = (k - a.first[t]) * kChunk, hi = min(a.count[t], lo + kChunk);
-    for (int64_t i = lo + threadIdx.x; i < hi; i += kNT) {
-      const float y = c * load_any(a, t, i);
-      if (a.bf16[t]) {
-        uint16_t h;
-        asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(y));
-        static_cast<uint16_t *>(a.out[t])[i] = h;
-      } else {
-        static_cast<float *>(a.out[t])[i] = y;
-      }
-    }
+    if (a.bf16[t])
+      scale_chunk<uint16_t>(a, t, chunk_of(a, t, k, 2), c);
+    else
+      scale_chunk<float>(a, t, chunk_of(a, t, k, 4), c);
   }
 }
 
 }  // namespace
 
-int64_t clip_chunks(const void *, int64_t count, int) { return (count + kChunk - 1) / kChunk; }
+int64_t clip_chunks(const void *in, int64_t count, int bf16) {
+  const int elem = bf16 ? 2 : 4;
+  const int64_t mis = (int64_t)(reinterpret_cast<uint64_t>(in) % 16) / elem;
+  return (mis + count + kChunkBytes / elem - 1) / (kChunkBytes / elem);
+}
 
 cudaError_t clip_norm_launch(const ClipArgs &a, int grid, cudaStream_t stream) {
   clip_norm_kernel<<<grid, kNT, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
-cudaError_t clip_scale_launch(const ClipArgs &a, int grid, cudaStream_t stream) {
-  clip_scale_kernel<<<grid, kNT, 0, stream>>>(a);
-  return cudaGetLastError();
+cudaError_t clip_scale_launch(const ClipArgs &a, int grid, bool after_norm, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid, 1, 1);
+  cfg.blockDim = dim3(kNT, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = after_norm ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, clip_scale_kernel, a);
 }
 
 }  // namespace specv

@@ -335,14 +335,16 @@ struct ClipArgs {
   int64_t chunks;            // chunks of this launch's tensors
   double *partial;
   float *out_norm;           // null except in one launch
+  int in_place;              // every out is its in
   const void *in[kClipTensors];
   void *out[kClipTensors];
   int64_t count[kClipTensors];   // elements
-  int64_t first[kClipTensors];   // the tensor's first chunk
+  int first[kClipTensors];       // the tensor's first chunk
   uint8_t bf16[kClipTensors];
 };
 int64_t clip_chunks(const void *in, int64_t count, int bf16);
 cudaError_t clip_norm_launch(const ClipArgs &a, int grid, cudaStream_t stream);
-cudaError_t clip_scale_launch(const ClipArgs &a, int grid, cudaStream_t stream);
+// after_norm: launched directly after clip_norm_launch, may begin while that drains
+cudaError_t clip_scale_launch(const ClipArgs &a, int grid, bool after_norm, cudaStream_t stream);
 
 }  // namespace specv

@@ -49,6 +49,9 @@ __device__ __forceinline__ uint16_t narrow<uint16_t>(float x) {
   return h;
 }
 
+__device__ __forceinline__ float widen(float x) { return x; }
+__device__ __forceinline__ float widen(uint16_t x) { return bf16_bits_to_float(x); }
+
 // ------------------------------------------------------- packed pairs of fp32
 // sm_103a adds, multiplies and fuses two fp32 values per instruction, each
 // rounded as its scalar form.
