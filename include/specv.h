@@ -564,7 +564,7 @@ typedef struct {
  * With c = 1 a gradient clipped in place is not written.  A norm that is not
  * finite leaves the values as they are (copied when out differs from grad), so
  * that a training loop can look at the norm and drop the step.  Squares are
- * summed in fp32 within 8192 elements and in fp64 beyond, in a fixed order; an
+ * summed in fp32 within 32 elements and to fp64 precision beyond, in a fixed order; an
  * element beyond 1.8e19 overflows its square and with it the norm.  No element
  * may be listed twice.  Scratch: at most 64 KiB in the stream's workspace (see
  * specv_verify).  Asynchronous on `stream`.

@@ -166,11 +166,11 @@ specv_status specv_clip_grads(const specv_grad *grads, int64_t n, float max_norm
   // One launch of each kernel per kClipTensors gradients; the sums of the norm's
   // launches lie one after the other.
   const int64_t groups = live > 0 ? (live + specv::kClipTensors - 1) / specv::kClipTensors : 1;
-  int per_launch = 4 * sms;
+  int per_launch = specv::kClipCtasPerSm * sms;
   if (groups * per_launch > specv::kClipPartials) per_launch = (int)(specv::kClipPartials / groups);
   if (per_launch < 1) return SPECV_ERR_INVALID_ARG;  // millions of gradients
   void *scratch = nullptr;
-  const size_t bytes = sizeof(double) * specv::kClipPartials;
+  const size_t bytes = sizeof(float2) * specv::kClipPartials;
   bool cached = false;
   try {
     cached = specv::stream_scratch(st, bytes, &scratch);
@@ -184,7 +184,7 @@ specv_status specv_clip_grads(const specv_grad *grads, int64_t n, float max_norm
     return SPECV_ERR_NO_MEMORY;
   }
   specv::ClipArgs a;
-  a.partial = static_cast<double *>(scratch);
+  a.partial = static_cast<float2 *>(scratch);
   a.max_norm = max_norm;
   for (int scale = 0; scale < 2; ++scale) {
     int64_t at = 0;

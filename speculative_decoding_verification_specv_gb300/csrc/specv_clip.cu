@@ -8,7 +8,7 @@
 // boundary, the last end after it; what is not the gradient's is not read), and
 // the chunks of all gradients are dealt to the CTAs in turn.  The first launch
 // sums squares, in fp32 within a thread's share of a chunk (two interleaved sums of
-// up to 32 terms) and in fp64 beyond; every CTA writes its sum.  Every CTA of the
+// up to 16 terms) and without further rounding beyond; every CTA writes its sum.  Every CTA of the
 // second launch adds those sums in the same order, so that all hold the same norm
 // (no atomics, one result), and scales its chunks, the last ones first: these the
 // first launch has left in L2.  The second launch begins while the first drains
@@ -22,7 +22,7 @@ namespace specv {
 namespace {
 
 constexpr int kNT = 256;
-constexpr int kVecs = 8;                              // 16-byte vectors per thread and chunk
+constexpr int kVecs = 4;                              // 16-byte vectors per thread and chunk
 constexpr int kChunkBytes = kNT * kVecs * 16;
 
 // The gradient that chunk k belongs to.
@@ -74,30 +74,40 @@ __device__ __forceinline__ uint64_t add_squares(uint64_t s, const uint4 &v) {
   return s;
 }
 
+// A thread's vectors of a chunk; what is not the gradient's is 0.
 template <typename T>
-__device__ __forceinline__ float chunk_squares(const Chunk &c) {
+__device__ __forceinline__ void load_chunk(const Chunk &c, uint4 (&v)[kVecs]) {
   constexpr int VW = Elem<T>::kPerVec;
-  uint4 v[kVecs];
+  const char *p = c.base + (int)threadIdx.x * 16;
   if (c.whole) {
-    const char *p = c.base + (int)threadIdx.x * 16;
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) v[u] = load16(p + u * (kNT * 16));
-  } else {
+    return;
+  }
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u) {
-      const int i = (int)threadIdx.x + u * kNT;
-      const int64_t first = c.at + (int64_t)i * VW;
-      v[u] = make_uint4(0, 0, 0, 0);
-      if (first >= 0 && first + VW <= c.count) {
-        v[u] = load16(c.base + (int64_t)i * 16);
-      } else if (first < c.count && first + VW > 0) {
-        const T *p = reinterpret_cast<const T *>(c.base + (int64_t)i * 16);
+  for (int u = 0; u < kVecs; ++u) {
+    const int64_t first = c.at + ((int64_t)threadIdx.x + u * kNT) * VW;
+    v[u] = make_uint4(0, 0, 0, 0);
+    if (first >= 0 && first + VW <= c.count) {
+      v[u] = load16(p + u * (kNT * 16));
+    } else if (first < c.count && first + VW > 0) {
+      const T *q = reinterpret_cast<const T *>(p + u * (kNT * 16));
 #pragma unroll
-        for (int e = 0; e < VW; ++e)
-          if (first + e >= 0 && first + e < c.count) Elem<T>::put_bits(v[u], e, Elem<T>::load_bits(p + e));
-      }
+      for (int e = 0; e < VW; ++e)
+        if (first + e >= 0 && first + e < c.count) {
+          if constexpr (sizeof(T) == 2)
+            Elem<T>::put_bits(v[u], e, q[e]);
+          else
+            Elem<T>::put_bits(v[u], e, __float_as_uint(q[e]));
+        }
     }
   }
+}
+
+template <typename T>
+__device__ __forceinline__ float chunk_squares(const Chunk &c) {
+  uint4 v[kVecs];
+  load_chunk<T>(c, v);
   uint64_t s = 0;
 #pragma unroll
   for (int u = 0; u < kVecs; ++u) s = add_squares<T>(s, v[u]);
@@ -106,28 +116,53 @@ __device__ __forceinline__ float chunk_squares(const Chunk &c) {
   return s0 + s1;
 }
 
-__device__ __forceinline__ double block_sum_d(double *red, double x) {
+// A sum as a pair of fp32, lo holding what hi rounds away (about 48 bits together).
+// fp64 additions run at 1/64 of the fp32 rate here: with them the CTAs' reductions
+// took longer than the reading (a draft head of 16 MB: 13 us a call).
+struct Sum {
+  float hi = 0.0f, lo = 0.0f;
+};
+__device__ __forceinline__ Sum operator+(const Sum &a, const Sum &b) {
+  Sum s;
+  s.hi = __fadd_rn(a.hi, b.hi);
+  const float part = __fsub_rn(s.hi, a.hi);
+  const float off = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s.hi, part)), __fsub_rn(b.hi, part));
+  // (an overflow leaves hi infinite; what it rounds away is then of no account)
+  s.lo = s.hi < INFINITY ? __fadd_rn(off, __fadd_rn(a.lo, b.lo)) : 0.0f;
+  return s;
+}
+// The CTA's sum in a fixed order, in every thread.
+__device__ __forceinline__ Sum block_sum(Sum *red, Sum x) {
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(~0u, x, off);
+  for (int off = 16; off > 0; off >>= 1) {
+    Sum y;
+    y.hi = __shfl_xor_sync(~0u, x.hi, off);
+    y.lo = __shfl_xor_sync(~0u, x.lo, off);
+    // (lanes take their pair in the same order: the sum is the same in both)
+    x = (threadIdx.x & off) == 0 ? x + y : y + x;
+  }
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
   __syncthreads();
-  x = 0.0;
+  x = red[0];
 #pragma unroll
-  for (int w = 0; w < kNT / 32; ++w) x += red[w];
+  for (int w = 1; w < kNT / 32; ++w) x = x + red[w];
   return x;
 }
 
-__global__ void __launch_bounds__(kNT, 4) clip_norm_kernel(const __grid_constant__ ClipArgs a) {
-  __shared__ double red[kNT / 32];
+__global__ void __launch_bounds__(kNT, kClipCtasPerSm)
+    clip_norm_kernel(const __grid_constant__ ClipArgs a) {
+  __shared__ Sum red[kNT / 32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  double sum = 0.0;
+  Sum sum;
   for (int64_t k = blockIdx.x; k < a.chunks; k += gridDim.x) {
     const int t = find_tensor(a, (int)k);
-    sum += (double)(a.bf16[t] ? chunk_squares<uint16_t>(chunk_of(a, t, (int)k, 2))
-                              : chunk_squares<float>(chunk_of(a, t, (int)k, 4)));
+    Sum x;
+    x.hi = a.bf16[t] ? chunk_squares<uint16_t>(chunk_of(a, t, (int)k, 2))
+                     : chunk_squares<float>(chunk_of(a, t, (int)k, 4));
+    sum = sum + x;
   }
-  sum = block_sum_d(red, sum);
-  if (threadIdx.x == 0) a.partial[a.partial_at + blockIdx.x] = sum;
+  sum = block_sum(red, sum);
+  if (threadIdx.x == 0) a.partial[a.partial_at + blockIdx.x] = make_float2(sum.hi, sum.lo);
 }
 
 // A vector's entries times c, rounded once.
@@ -146,34 +181,46 @@ __device__ __forceinline__ uint4 scaled(const uint4 &v, uint64_t c) {
 template <typename T>
 __device__ __forceinline__ void scale_chunk(const ClipArgs &a, int t, const Chunk &c, float factor) {
   constexpr int VW = Elem<T>::kPerVec;
-  const T *in = static_cast<const T *>(a.in[t]);
   T *out = static_cast<T *>(a.out[t]);
   const uint64_t f = pack2(factor, factor);
   // vectors where the output lies as the input against the 16-byte boundaries
-  const bool alike = (reinterpret_cast<uint64_t>(in) - reinterpret_cast<uint64_t>(out)) % 16 == 0;
+  const bool alike = (reinterpret_cast<uint64_t>(a.in[t]) - reinterpret_cast<uint64_t>(out)) % 16 == 0;
+  uint4 v[kVecs];
+  load_chunk<T>(c, v);
+#pragma unroll
+  for (int u = 0; u < kVecs; ++u) v[u] = scaled<T>(v[u], f);
+  T *q = out + c.at + (int)threadIdx.x * VW;
   if (alike && c.whole) {
-    uint4 v[kVecs];
-    const char *p = c.base + (int)threadIdx.x * 16;
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u) v[u] = load16(p + u * (kNT * 16));
-    uint4 *q = reinterpret_cast<uint4 *>(out + c.at) + threadIdx.x;
-#pragma unroll
-    for (int u = 0; u < kVecs; ++u) q[u * kNT] = scaled<T>(v[u], f);
+    for (int u = 0; u < kVecs; ++u) *reinterpret_cast<uint4 *>(q + u * (kNT * VW)) = v[u];
     return;
   }
-  const int64_t lo = c.at < 0 ? 0 : c.at, end = c.at + (int64_t)kNT * kVecs * VW;
-  const int64_t hi = end < c.count ? end : c.count;
-#pragma unroll 4
-  for (int64_t i = lo + threadIdx.x; i < hi; i += kNT)
-    out[i] = narrow<T>(__fmul_rn(factor, widen(in[i])));
+#pragma unroll
+  for (int u = 0; u < kVecs; ++u) {
+    const int64_t first = c.at + ((int64_t)threadIdx.x + u * kNT) * VW;
+    if (alike && first >= 0 && first + VW <= c.count) {
+      *reinterpret_cast<uint4 *>(q + u * (kNT * VW)) = v[u];
+    } else {
+#pragma unroll
+      for (int e = 0; e < VW; ++e)
+        if (first + e >= 0 && first + e < c.count) q[u * (kNT * VW) + e] = narrow<T>(Elem<T>::get(v[u], e));
+    }
+  }
 }
 
-__global__ void __launch_bounds__(kNT, 4) clip_scale_kernel(const __grid_constant__ ClipArgs a) {
-  __shared__ double red[kNT / 32];
+__global__ void __launch_bounds__(kNT, kClipCtasPerSm)
+    clip_scale_kernel(const __grid_constant__ ClipArgs a) {
+  __shared__ Sum red[kNT / 32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  double sum = 0.0;
-  for (int i = threadIdx.x; i < a.partials; i += kNT) sum += a.partial[i];
-  const float norm = (float)sqrt(block_sum_d(red, sum));
+  Sum sum;
+  for (int i = threadIdx.x; i < a.partials; i += kNT) {
+    Sum x;
+    x.hi = a.partial[i].x;
+    x.lo = a.partial[i].y;
+    sum = sum + x;
+  }
+  sum = block_sum(red, sum);
+  const float norm = sqrtf(__fadd_rn(sum.hi, sum.lo));
   if (a.out_norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *a.out_norm = norm;
   // a norm that is not finite gives no factor: the values are left as they are
   const float c = norm < INFINITY ? fminf(1.0f, a.max_norm / (norm + kClipEps)) : 1.0f;

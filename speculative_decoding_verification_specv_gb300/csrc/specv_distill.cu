@@ -197,6 +197,7 @@ __device__ __forceinline__ void gradient(const GradTerms &g, const TileT &xt, Ti
 // ------------------------------------------------------------------- short rows
 // One CTA of 64 threads per pair, at most two register tiles of it.
 constexpr int kSmallNT = 64;
+constexpr int kPackUnroll = 2;  // packs per lane of a tile
 
 template <typename T, bool SHIFTED, bool REVERSE>
 __global__ void __launch_bounds__(kSmallNT) distill_short_kernel(DistillArgs a) {
@@ -224,7 +225,7 @@ __global__ void __launch_bounds__(kSmallNT) distill_short_kernel(DistillArgs a) 
   }
   const GridRow<T, SHIFTED> rt(zt, grid), rq(zq, grid);
   constexpr int kTile = kPackUnroll * kSmallNT;
-  PackTile<T, SHIFTED> xt[2], xq[2];
+  PackTile<T, SHIFTED, kPackUnroll> xt[2], xq[2];
   PairSums x;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -298,13 +299,13 @@ struct ChunkTile {
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j) {
       const int k = k0 + j * kNT + (int)threadIdx.x;
-      v[j] = PackTile<T, SHIFTED>::none();
+      v[j] = PackTile<T, SHIFTED, 1>::none();
       if (k >= end) continue;
       if (k >= r.lo && k < r.hi) {
         v[j] = p[j * kNT];
         if (SHIFTED && r.shift != 0) v[j] = shifted<T>(v[j], p[j * kNT + 1], r.shift);
       } else if (SHIFTED) {
-        v[j] = PackTile<T, SHIFTED>::load_entries(r.row, (int64_t)k * VW - grid.mis, grid.V);
+        v[j] = PackTile<T, SHIFTED, 1>::load_entries(r.row, (int64_t)k * VW - grid.mis, grid.V);
       }
     }
   }

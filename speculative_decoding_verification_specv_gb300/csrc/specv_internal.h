@@ -324,7 +324,8 @@ cudaError_t distill_launch(const DistillArgs &a, int dtype_bf16, int reverse, in
 
 // Arguments of the clipping kernels: up to kClipTensors gradients per launch,
 // passed by value in the parameter space (no table to copy to the device).
-constexpr int kClipTensors = 400;
+constexpr int kClipTensors = 1000;
+constexpr int kClipCtasPerSm = 4;
 constexpr float kClipEps = 1e-6f;
 constexpr int kClipPartials = 8192;  // sums of squares of one call (64 KiB of scratch)
 struct ClipArgs {
@@ -333,7 +334,7 @@ struct ClipArgs {
   int partial_at;            // where this launch's sums begin
   float max_norm;
   int64_t chunks;            // chunks of this launch's tensors
-  double *partial;
+  float2 *partial;           // (sum, what it rounds away)
   float *out_norm;           // null except in one launch
   int in_place;              // every out is its in
   const void *in[kClipTensors];

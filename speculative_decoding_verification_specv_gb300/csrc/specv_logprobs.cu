@@ -318,31 +318,74 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 1024 / NT)
   }
 }
 
-constexpr int kNT = 256;
+// ------------------------------------------------------------------ the gradient
+//   dz_v = g (1[v = x] - p_v) - h p_v (ln p_v + H)
+// from the statistics of the forward pass: each entry is read and its gradient
+// written once.  A warp takes kGradUnroll packs per lane of one row, on the grid of
+// the output's row.
+constexpr int kGradNT = 256;
+constexpr int kGradUnroll = 4;
+constexpr int kGradUnit = 32 * kGradUnroll;  // packs of a warp's share
 
-// dz_v = g (1[v = x] - p_v) - h p_v (ln p_v + H): one CTA per row.
-template <typename T>
-__global__ void __launch_bounds__(kNT) logprobs_grad_kernel(LogprobGradArgs a) {
-  const int64_t r = blockIdx.x;
-  const int V = a.V;
+template <typename T, bool SHIFTED>
+__global__ void __launch_bounds__(kGradNT) logprobs_grad_kernel(LogprobGradArgs a, uint32_t units) {
+  constexpr int VW = Elem<T>::kPerVec;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint64_t unit = (uint64_t)blockIdx.x * (kGradNT / 32) + warp;  // share `unit % units` of row
+  const int64_t r = unit >> 32 == 0 ? (uint32_t)unit / units : unit / units;
+  if (r >= a.R) return;
+  const int k0 = (int)(unit - (uint64_t)r * units) * kGradUnit;
   const T *row = static_cast<const T *>(a.logits) + row_offset(r, a.N, a.stride_b, a.stride_n);
-  T *out = static_cast<T *>(a.out) + r * (int64_t)V;
+  T *out = static_cast<T *>(a.out) + r * (int64_t)a.V;
+  const Grid<T> grid(out, a.V);
   const int32_t x = a.tokens[r];
   const float2 st = a.stats[r];
-  const float H = a.entropy[r], g = a.grad_logprob[r];
+  const float g = a.grad_logprob[r], H = a.entropy[r];
   const float h = a.grad_entropy != nullptr ? a.grad_entropy[r] : 0.0f;
-  const bool zero = x == -1 || st.x == -INFINITY;
-  const bool bad = x < -1 || x >= V;
-  for (int64_t v = threadIdx.x; v < V; v += kNT) {
-    float d = 0.0f;
-    if (bad) {
-      d = quiet_nan();
-    } else if (!zero) {
-      const float lp = (Elem<T>::load(row + v) - st.x) - st.y;
-      const float p = ex2(lp * kLog2e);
-      d = (v == x ? g : 0.0f) - p * (g + h * (fmaxf(lp, kFarBelow) + H));
+  const bool bad = x < -1 || x >= a.V;
+  const bool zero = x == -1 || (!bad && st.x == -INFINITY);
+  PackTile<T, SHIFTED, kGradUnroll> z;
+  if (zero || bad) {
+    const float fill = zero ? 0.0f : quiet_nan();
+#pragma unroll
+    for (int i = 0; i < z.kPairs; ++i) z.put(i, fill, fill);
+#pragma unroll
+    for (int j = 0; j < kGradUnroll; ++j) {
+      const int k = k0 + 32 * j + lane;
+      if (k < grid.count) store_pack<T>(out, grid, k, z.v[j]);
     }
-    out[v] = narrow<T>(d);
+    return;
+  }
+  const GridRow<T, SHIFTED> from(row, grid);
+  z.load(from, grid, k0, grid.count);
+  // the lane that holds the token's entry
+  const int64_t kx = ((int64_t)x + grid.mis) / VW;
+  const bool mine = kx >= k0 && kx < k0 + kGradUnit && ((int)(kx - k0) & 31) == lane;
+  float zx = 0.0f;
+  if (mine) zx = widen(*reinterpret_cast<const volatile T *>(row + x));
+  z.join(from);
+
+  const uint64_t m2 = pack2(-st.x, -st.x), l2 = pack2(-st.y, -st.y), scale = pack2(kLog2e, kLog2e);
+  const float c = -__fmaf_rn(h, H, g);  // out = p (c - h ln p)
+  const uint64_t c2 = pack2(c, c), h2 = pack2(-h, -h);
+#pragma unroll
+  for (int i = 0; i < z.kPairs; ++i) {
+    const uint64_t lp = add2(add2(z.pair(i), m2), l2);
+    float l0, l1, e0, e1, d0, d1;
+    unpack2(lp, l0, l1);
+    unpack2(mul2(lp, scale), e0, e1);
+    const uint64_t in = fma2(h2, pack2(fmaxf(l0, kFarBelow), fmaxf(l1, kFarBelow)), c2);
+    unpack2(mul2(pack2(ex2(e0), ex2(e1)), in), d0, d1);
+    z.put(i, d0, d1);
+  }
+#pragma unroll
+  for (int j = 0; j < kGradUnroll; ++j) {
+    const int k = k0 + 32 * j + lane;
+    if (k < grid.count) store_pack<T>(out, grid, k, z.v[j]);
+  }
+  if (mine) {
+    const float lp = (zx - st.x) - st.y;
+    out[x] = narrow<T>(__fmaf_rn(ex2(lp * kLog2e), __fmaf_rn(-h, fmaxf(lp, kFarBelow), c), g));
   }
 }
 
@@ -394,12 +437,27 @@ cudaError_t logprobs_launch(const LogprobArgs &a, int dtype_bf16, int sms, int S
   return dtype_bf16 ? forward<uint16_t>(a, sms, S, stream) : forward<float>(a, sms, S, stream);
 }
 
-cudaError_t logprobs_grad_launch(const LogprobGradArgs &a, int dtype_bf16, cudaStream_t stream) {
-  if (dtype_bf16)
-    logprobs_grad_kernel<uint16_t><<<(unsigned)a.R, kNT, 0, stream>>>(a);
-  else
-    logprobs_grad_kernel<float><<<(unsigned)a.R, kNT, 0, stream>>>(a);
+template <typename T, bool SHIFTED>
+static cudaError_t launch_grad(const LogprobGradArgs &a, cudaStream_t stream) {
+  constexpr int VW = Elem<T>::kPerVec;
+  // shares of a row, wherever it begins
+  const int64_t packs = ((int64_t)a.V + (SHIFTED ? 2 : 1) * (VW - 1)) / VW;
+  const int64_t units = (packs + kGradUnit - 1) / kGradUnit;
+  const int64_t ctas = (a.R * units + kGradNT / 32 - 1) / (kGradNT / 32);
+  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+  logprobs_grad_kernel<T, SHIFTED><<<(unsigned)ctas, kGradNT, 0, stream>>>(a, (uint32_t)units);
   return cudaGetLastError();
+}
+
+cudaError_t logprobs_grad_launch(const LogprobGradArgs &a, int dtype_bf16, cudaStream_t stream) {
+  // Every row of both arrays begins on a 16-byte boundary where their addresses, the
+  // strides and V in bytes are multiples of 16.
+  const uint64_t bits = reinterpret_cast<uint64_t>(a.logits) | reinterpret_cast<uint64_t>(a.out) |
+                        (uint64_t)(a.stride_b | a.stride_n | a.V) * (dtype_bf16 ? 2 : 4);
+  if (dtype_bf16)
+    return bits % 16 == 0 ? launch_grad<uint16_t, false>(a, stream)
+                          : launch_grad<uint16_t, true>(a, stream);
+  return bits % 16 == 0 ? launch_grad<float, false>(a, stream) : launch_grad<float, true>(a, stream);
 }
 
 }  // namespace specv

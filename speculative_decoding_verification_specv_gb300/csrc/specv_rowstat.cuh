@@ -211,11 +211,10 @@ __device__ __forceinline__ uint64_t warp_merge(uint64_t a, uint64_t b) {
 }
 
 // ------------------------------------------------------ rows on another row's grid
-// A warp's share of a row, kU 16-byte packs per lane, on the grid of a row that
-// may sit differently against the 16-byte boundaries (the row of a contiguous
-// output, say, whose width no vector divides): pack k of the grid covers entries
+// A warp's share of a row, U 16-byte packs per lane, on the grid of a row that may
+// sit differently against the 16-byte boundaries (the row of a contiguous output,
+// say, whose width no vector divides): pack k of the grid covers entries
 // [k VW - mis, (k + 1) VW - mis).  Lane l's j-th pack is k0 + 32 j + l.
-constexpr int kPackUnroll = 2;
 
 template <typename T>
 struct Grid {
@@ -304,10 +303,10 @@ __device__ __forceinline__ void put_pair(uint4 &x, int i, float a, float b) {
   }
 }
 
-template <typename T, bool SHIFTED>
+template <typename T, bool SHIFTED, int U>
 struct PackTile {
-  static constexpr int kPairs = kPackUnroll * Elem<T>::kPerVec / 2;  // packed pairs of entries
-  uint4 v[kPackUnroll + (SHIFTED ? 1 : 0)];
+  static constexpr int kPairs = U * Elem<T>::kPerVec / 2;  // packed pairs of entries
+  uint4 v[U + (SHIFTED ? 1 : 0)];
   bool joined;  // the packs are whole (else v holds vectors still to be joined)
 
   __device__ __forceinline__ static uint4 load16(const char *p) {
@@ -347,20 +346,20 @@ struct PackTile {
                                        int end) {
     constexpr int VW = Elem<T>::kPerVec;
     const int lane = threadIdx.x & 31;
-    if (k0 >= r.lo && k0 + 32 * kPackUnroll <= min(r.hi, end)) {
+    if (k0 >= r.lo && k0 + 32 * U <= min(r.hi, end)) {
       const char *p = r.base + ((int64_t)k0 + lane) * 16;
 #pragma unroll
-      for (int j = 0; j < kPackUnroll; ++j) v[j] = load16(p + j * 512);
+      for (int j = 0; j < U; ++j) v[j] = load16(p + j * 512);
       if (SHIFTED) {
         joined = r.shift == 0;
         // lane 31's second vector of the last pack, fetched by lane 0
-        if (!joined && lane == 0) v[kPackUnroll] = load16(p + kPackUnroll * 512);
+        if (!joined && lane == 0) v[U] = load16(p + U * 512);
       }
       return;
     }
     joined = true;
 #pragma unroll
-    for (int j = 0; j < kPackUnroll; ++j) {
+    for (int j = 0; j < U; ++j) {
       const int k = k0 + 32 * j + lane;
       v[j] = none();
       if (k < end) {
@@ -377,7 +376,7 @@ struct PackTile {
     if (!SHIFTED || joined) return;
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int j = 0; j < kPackUnroll; ++j) {
+    for (int j = 0; j < U; ++j) {
       const uint4 &n = v[j + 1];
       uint4 next;  // the next lane's vector; lane 31's is the next pack's first
       next.x = __shfl_sync(0xffffffffu, lane == 0 ? n.x : v[j].x, (lane + 1) & 31);
@@ -396,7 +395,7 @@ struct PackTile {
   __device__ __forceinline__ float largest() const {
     float m = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < kPackUnroll; ++j) m = fmaxf(m, vector_max<T>(v[j]));
+    for (int j = 0; j < U; ++j) m = fmaxf(m, vector_max<T>(v[j]));
     return m;
   }
   __device__ __forceinline__ void put(int i, float a, float b) {
