@@ -41,6 +41,49 @@ bool misaligned(const void *p, int64_t dtype) {
   return (uintptr_t)p % (dtype == SPECV_BF16 ? 2 : 4) != 0;
 }
 
+// The launches of specv_clip_grads: the norm's, then the scaling's, each for up to CAP
+// gradients.
+template <int CAP>
+cudaError_t clip_launches(const specv_grad *grads, int64_t n, float max_norm, float *out_norm,
+                          float2 *partial, int64_t groups, int per_launch, cudaStream_t st) {
+  cudaError_t e = cudaSuccess;
+  specv::ClipArgs<CAP> a;
+  a.partial = partial;
+  a.max_norm = max_norm;
+  for (int scale = 0; scale < 2; ++scale) {
+    int64_t at = 0;
+    int partials = 0;
+    for (int64_t g = 0; g < groups && e == cudaSuccess; ++g) {
+      a.n = 0;
+      a.chunks = 0;
+      a.in_place = 1;
+      for (; at < n && a.n < CAP; ++at) {
+        if (grads[at].count == 0) continue;
+        const int k = a.n++;
+        a.in_place &= grads[at].out == grads[at].grad;
+        a.in[k] = grads[at].grad;
+        a.out[k] = grads[at].out;
+        a.count[k] = grads[at].count;
+        a.bf16[k] = grads[at].dtype == SPECV_BF16;
+        a.first[k] = (int)a.chunks;
+        a.chunks += specv::clip_chunks(a.in[k], a.count[k], a.bf16[k]);
+      }
+      int grid = a.chunks < per_launch ? (int)a.chunks : per_launch;
+      if (grid < 1) grid = 1;
+      a.out_norm = g == 0 ? out_norm : nullptr;
+      if (scale == 0) {
+        a.partial_at = partials;
+        partials += grid;
+        a.partials = partials;
+        e = specv::clip_norm_launch(a, grid, st);
+      } else {
+        e = specv::clip_scale_launch(a, grid, g == 0, st);
+      }
+    }
+  }
+  return e;
+}
+
 }  // namespace
 
 extern "C" {
@@ -163,9 +206,9 @@ specv_status specv_clip_grads(const specv_grad *grads, int64_t n, float max_norm
   const int ready = specv::device_ready(&sms);
   if (ready != SPECV_OK) return (specv_status)ready;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // One launch of each kernel per kClipTensors gradients; the sums of the norm's
-  // launches lie one after the other.
-  const int64_t groups = live > 0 ? (live + specv::kClipTensors - 1) / specv::kClipTensors : 1;
+  // One launch of each kernel per kClipMany gradients; the sums of the norm's launches
+  // lie one after the other.
+  const int64_t groups = live > 0 ? (live + specv::kClipMany - 1) / specv::kClipMany : 1;
   int per_launch = specv::kClipCtasPerSm * sms;
   if (groups * per_launch > specv::kClipPartials) per_launch = (int)(specv::kClipPartials / groups);
   if (per_launch < 1) return SPECV_ERR_INVALID_ARG;  // millions of gradients
@@ -183,40 +226,13 @@ specv_status specv_clip_grads(const specv_grad *grads, int64_t n, float max_norm
     (void)cudaGetLastError();
     return SPECV_ERR_NO_MEMORY;
   }
-  specv::ClipArgs a;
-  a.partial = static_cast<float2 *>(scratch);
-  a.max_norm = max_norm;
-  for (int scale = 0; scale < 2; ++scale) {
-    int64_t at = 0;
-    int partials = 0;
-    for (int64_t g = 0; g < groups && e == cudaSuccess; ++g) {
-      a.n = 0;
-      a.chunks = 0;
-      a.in_place = 1;
-      for (; at < n && a.n < specv::kClipTensors; ++at) {
-        if (grads[at].count == 0) continue;
-        const int k = a.n++;
-        a.in_place &= grads[at].out == grads[at].grad;
-        a.in[k] = grads[at].grad;
-        a.out[k] = grads[at].out;
-        a.count[k] = grads[at].count;
-        a.bf16[k] = grads[at].dtype == SPECV_BF16;
-        a.first[k] = (int)a.chunks;
-        a.chunks += specv::clip_chunks(a.in[k], a.count[k], a.bf16[k]);
-      }
-      int grid = a.chunks < per_launch ? (int)a.chunks : per_launch;
-      if (grid < 1) grid = 1;
-      a.out_norm = g == 0 ? out_norm : nullptr;
-      if (scale == 0) {
-        a.partial_at = partials;
-        partials += grid;
-        a.partials = partials;
-        e = specv::clip_norm_launch(a, grid, st);
-      } else {
-        e = specv::clip_scale_launch(a, grid, g == 0, st);
-      }
-    }
-  }
+  float2 *partial = static_cast<float2 *>(scratch);
+  if (e == cudaSuccess)
+    e = live <= specv::kClipFew
+            ? clip_launches<specv::kClipFew>(grads, n, max_norm, out_norm, partial, groups,
+                                             per_launch, st)
+            : clip_launches<specv::kClipMany>(grads, n, max_norm, out_norm, partial, groups,
+                                              per_launch, st);
   if (!cached) {
     const cudaError_t ef = cudaFreeAsync(scratch, st);
     if (e == cudaSuccess) e = ef;

@@ -26,7 +26,8 @@ constexpr int kVecs = 4;                              // 16-byte vectors per thr
 constexpr int kChunkBytes = kNT * kVecs * 16;
 
 // The gradient that chunk k belongs to.
-__device__ __forceinline__ int find_tensor(const ClipArgs &a, int k) {
+template <typename Args>
+__device__ __forceinline__ int find_tensor(const Args &a, int k) {
   int lo = 0, hi = a.n - 1;  // the last one that begins at or before the chunk
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -51,7 +52,8 @@ struct Chunk {
   int64_t at, count;
   bool whole;  // every vector lies within the gradient
 };
-__device__ __forceinline__ Chunk chunk_of(const ClipArgs &a, int t, int k, int elem) {
+template <typename Args>
+__device__ __forceinline__ Chunk chunk_of(const Args &a, int t, int k, int elem) {
   const uint64_t p = reinterpret_cast<uint64_t>(a.in[t]);
   const int mis = (int)(p % 16) / elem, per_vec = 16 / elem;
   Chunk c;
@@ -149,8 +151,9 @@ __device__ __forceinline__ Sum block_sum(Sum *red, Sum x) {
   return x;
 }
 
+template <int CAP>
 __global__ void __launch_bounds__(kNT, kClipCtasPerSm)
-    clip_norm_kernel(const __grid_constant__ ClipArgs a) {
+    clip_norm_kernel(const __grid_constant__ ClipArgs<CAP> a) {
   __shared__ Sum red[kNT / 32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Sum sum;
@@ -179,12 +182,13 @@ __device__ __forceinline__ uint4 scaled(const uint4 &v, uint64_t c) {
 }
 
 template <typename T>
-__device__ __forceinline__ void scale_chunk(const ClipArgs &a, int t, const Chunk &c, float factor) {
+__device__ __forceinline__ void scale_chunk(const void *from, void *to, const Chunk &c,
+                                            float factor) {
   constexpr int VW = Elem<T>::kPerVec;
-  T *out = static_cast<T *>(a.out[t]);
+  T *out = static_cast<T *>(to);
   const uint64_t f = pack2(factor, factor);
   // vectors where the output lies as the input against the 16-byte boundaries
-  const bool alike = (reinterpret_cast<uint64_t>(a.in[t]) - reinterpret_cast<uint64_t>(out)) % 16 == 0;
+  const bool alike = (reinterpret_cast<uint64_t>(from) - reinterpret_cast<uint64_t>(out)) % 16 == 0;
   uint4 v[kVecs];
   load_chunk<T>(c, v);
 #pragma unroll
@@ -208,8 +212,9 @@ __device__ __forceinline__ void scale_chunk(const ClipArgs &a, int t, const Chun
   }
 }
 
+template <int CAP>
 __global__ void __launch_bounds__(kNT, kClipCtasPerSm)
-    clip_scale_kernel(const __grid_constant__ ClipArgs a) {
+    clip_scale_kernel(const __grid_constant__ ClipArgs<CAP> a) {
   __shared__ Sum red[kNT / 32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   Sum sum;
@@ -229,9 +234,9 @@ __global__ void __launch_bounds__(kNT, kClipCtasPerSm)
     const int k = (int)j, t = find_tensor(a, k);
     if (c == 1.0f && a.out[t] == a.in[t]) continue;
     if (a.bf16[t])
-      scale_chunk<uint16_t>(a, t, chunk_of(a, t, k, 2), c);
+      scale_chunk<uint16_t>(a.in[t], a.out[t], chunk_of(a, t, k, 2), c);
     else
-      scale_chunk<float>(a, t, chunk_of(a, t, k, 4), c);
+      scale_chunk<float>(a.in[t], a.out[t], chunk_of(a, t, k, 4), c);
   }
 }
 
@@ -243,12 +248,15 @@ int64_t clip_chunks(const void *in, int64_t count, int bf16) {
   return (mis + count + kChunkBytes / elem - 1) / (kChunkBytes / elem);
 }
 
-cudaError_t clip_norm_launch(const ClipArgs &a, int grid, cudaStream_t stream) {
-  clip_norm_kernel<<<grid, kNT, 0, stream>>>(a);
+template <int CAP>
+cudaError_t clip_norm_launch(const ClipArgs<CAP> &a, int grid, cudaStream_t stream) {
+  clip_norm_kernel<CAP><<<grid, kNT, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
-cudaError_t clip_scale_launch(const ClipArgs &a, int grid, bool after_norm, cudaStream_t stream) {
+template <int CAP>
+cudaError_t clip_scale_launch(const ClipArgs<CAP> &a, int grid, bool after_norm,
+                              cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid, 1, 1);
   cfg.blockDim = dim3(kNT, 1, 1);
@@ -258,7 +266,12 @@ cudaError_t clip_scale_launch(const ClipArgs &a, int grid, bool after_norm, cuda
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = after_norm ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, clip_scale_kernel, a);
+  return cudaLaunchKernelEx(&cfg, clip_scale_kernel<CAP>, a);
 }
+
+template cudaError_t clip_norm_launch(const ClipArgs<kClipFew> &, int, cudaStream_t);
+template cudaError_t clip_norm_launch(const ClipArgs<kClipMany> &, int, cudaStream_t);
+template cudaError_t clip_scale_launch(const ClipArgs<kClipFew> &, int, bool, cudaStream_t);
+template cudaError_t clip_scale_launch(const ClipArgs<kClipMany> &, int, bool, cudaStream_t);
 
 }  // namespace specv

@@ -322,30 +322,38 @@ cudaError_t distill_prepare();
 cudaError_t distill_launch(const DistillArgs &a, int dtype_bf16, int reverse, int S,
                            cudaStream_t stream);
 
-// Arguments of the clipping kernels: up to kClipTensors gradients per launch,
-// passed by value in the parameter space (no table to copy to the device).
-constexpr int kClipTensors = 1000;
+// Arguments of the clipping kernels: up to CAP gradients per launch, passed by value
+// in the parameter space (no table to copy to the device).  Two capacities: the
+// host's part of a launch grows with the parameters' size (a call with 14 gradients
+// takes 24 us of host time with room for 1000 in each of its launches, 22 with 64;
+// the kernels take the same).
+constexpr int kClipFew = 64;
+constexpr int kClipMany = 1000;  // 29 KB of the 32 KB a launch may carry
 constexpr int kClipCtasPerSm = 4;
 constexpr float kClipEps = 1e-6f;
 constexpr int kClipPartials = 8192;  // sums of squares of one call (64 KiB of scratch)
+template <int CAP>
 struct ClipArgs {
-  int n;                     // tensors of this launch
+  int n;                     // gradients of this launch
   int partials;              // sums written by all launches of the norm
   int partial_at;            // where this launch's sums begin
+  int in_place;              // every out is its in
   float max_norm;
-  int64_t chunks;            // chunks of this launch's tensors
+  int64_t chunks;            // chunks of this launch's gradients
   float2 *partial;           // (sum, what it rounds away)
   float *out_norm;           // null except in one launch
-  int in_place;              // every out is its in
-  const void *in[kClipTensors];
-  void *out[kClipTensors];
-  int64_t count[kClipTensors];   // elements
-  int first[kClipTensors];       // the tensor's first chunk
-  uint8_t bf16[kClipTensors];
+  const void *in[CAP];
+  void *out[CAP];
+  int64_t count[CAP];        // elements
+  int first[CAP];            // the gradient's first chunk
+  uint8_t bf16[CAP];
 };
 int64_t clip_chunks(const void *in, int64_t count, int bf16);
-cudaError_t clip_norm_launch(const ClipArgs &a, int grid, cudaStream_t stream);
+template <int CAP>
+cudaError_t clip_norm_launch(const ClipArgs<CAP> &a, int grid, cudaStream_t stream);
 // after_norm: launched directly after clip_norm_launch, may begin while that drains
-cudaError_t clip_scale_launch(const ClipArgs &a, int grid, bool after_norm, cudaStream_t stream);
+template <int CAP>
+cudaError_t clip_scale_launch(const ClipArgs<CAP> &a, int grid, bool after_norm,
+                              cudaStream_t stream);
 
 }  // namespace specv

@@ -9,12 +9,13 @@ others have any strides (rows of a padded vocabulary, ``target_logits[:, :K]``).
 """
 from __future__ import annotations
 
-import ctypes
+from array import array
+from operator import attrgetter
 from typing import NamedTuple, Optional
 
 import torch
 
-from . import _check, _dtype_code, _require, _stream_ptr, load
+from . import BF16, F32, _check, _dtype_code, _require, load
 
 FORWARD_KL = 0  # KL(target || draft)
 REVERSE_KL = 1  # KL(draft || target)
@@ -31,6 +32,33 @@ class TokenLogprobs(NamedTuple):
     top_logprobs: Optional[torch.Tensor]
 
 
+# These calls are short enough on the GPU that the host's part of one counts: entry
+# points are looked up once, a tensor that fits is passed with a single test, and the
+# stream's handle is asked for without building a Stream object.
+_CODES = {torch.float32: F32, torch.bfloat16: BF16}
+_entries: dict = {}
+
+
+def _entry(name: str):
+    fn = _entries.get(name)
+    if fn is None:
+        fn = _entries[name] = getattr(load(), name)
+    return fn
+
+
+def _stream(stream, dev) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _fit(t, name: str, dtype, shape, dev):
+    """A contiguous tensor of this type, shape and device, else the error that says why."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.device == dev and t.is_contiguous()):
+        _require(t, name, dtype, shape, dev)
+
+
 def _rows(t: torch.Tensor, name: str):
     """(B, N, V, stride_b, stride_n) of logits [B][N][V] or [N][V] on the GPU."""
     if not isinstance(t, torch.Tensor):
@@ -42,7 +70,7 @@ def _rows(t: torch.Tensor, name: str):
         B, sb = 1, 0
     else:
         raise ValueError(f"{name} must be [B][N][V] or [N][V]")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (the kernels run only on the GPU)")
     if sv != 1 and V > 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
@@ -64,7 +92,7 @@ def token_logprobs(logits, tokens, top_n: int = 0, stream=None) -> TokenLogprobs
     B, N, V, sb, sn = _rows(logits, "logits")
     dev, lead = logits.device, logits.shape[:-1]
     code = _dtype_code(logits)
-    _require(tokens, "tokens", torch.int32, lead, dev)
+    _fit(tokens, "tokens", torch.int32, lead, dev)
     n = int(top_n)
     if not 0 <= n <= MAX_TOP:
         raise ValueError(f"top_n must be in 0..{MAX_TOP}")
@@ -75,11 +103,12 @@ def token_logprobs(logits, tokens, top_n: int = 0, stream=None) -> TokenLogprobs
     if n:
         top_t = torch.empty((*lead, n), dtype=torch.int32, device=dev)
         top_l = torch.empty((*lead, n), dtype=torch.float32, device=dev)
-    st = load().specv_token_logprobs(
+    st = _entry("specv_token_logprobs")(
         logits.data_ptr(), tokens.data_ptr(), B, N, V, sb, sn, code, n, logprobs.data_ptr(),
         entropy.data_ptr(), stats.data_ptr(), top_t.data_ptr() if n else None,
-        top_l.data_ptr() if n else None, _stream_ptr(stream, dev))
-    _check(st, "specv_token_logprobs")
+        top_l.data_ptr() if n else None, _stream(stream, dev))
+    if st:
+        _check(st, "specv_token_logprobs")
     return TokenLogprobs(logprobs, entropy, stats, top_t, top_l)
 
 
@@ -96,21 +125,22 @@ def token_logprobs_backward(logits, tokens, stats, entropy, grad_logprobs, grad_
     B, N, V, sb, sn = _rows(logits, "logits")
     dev, lead = logits.device, logits.shape[:-1]
     code = _dtype_code(logits)
-    _require(tokens, "tokens", torch.int32, lead, dev)
-    _require(stats, "stats", torch.float32, (*lead, 2), dev)
-    _require(entropy, "entropy", torch.float32, lead, dev)
-    _require(grad_logprobs, "grad_logprobs", torch.float32, lead, dev)
+    _fit(tokens, "tokens", torch.int32, lead, dev)
+    _fit(stats, "stats", torch.float32, (*lead, 2), dev)
+    _fit(entropy, "entropy", torch.float32, lead, dev)
+    _fit(grad_logprobs, "grad_logprobs", torch.float32, lead, dev)
     if grad_entropy is not None:
-        _require(grad_entropy, "grad_entropy", torch.float32, lead, dev)
+        _fit(grad_entropy, "grad_entropy", torch.float32, lead, dev)
     if out is None:
         out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
     else:
-        _require(out, "out", logits.dtype, logits.shape, dev)
-    st = load().specv_token_logprobs_backward(
+        _fit(out, "out", logits.dtype, logits.shape, dev)
+    st = _entry("specv_token_logprobs_backward")(
         logits.data_ptr(), tokens.data_ptr(), stats.data_ptr(), entropy.data_ptr(),
         grad_logprobs.data_ptr(), None if grad_entropy is None else grad_entropy.data_ptr(), B, N,
-        V, sb, sn, code, out.data_ptr(), _stream_ptr(stream, dev))
-    _check(st, "specv_token_logprobs_backward")
+        V, sb, sn, code, out.data_ptr(), _stream(stream, dev))
+    if st:
+        _check(st, "specv_token_logprobs_backward")
     return out
 
 
@@ -140,20 +170,21 @@ def distill(target_logits, draft_logits, weight=None, kind: int = FORWARD_KL, ne
     if target_logits.dtype != draft_logits.dtype:
         raise TypeError(f"target_logits must be {draft_logits.dtype}, got {target_logits.dtype}")
     if weight is not None:
-        _require(weight, "weight", torch.float32, (B, K), dev)
+        _fit(weight, "weight", torch.float32, (B, K), dev)
     if kind not in (FORWARD_KL, REVERSE_KL):
         raise ValueError("kind must be FORWARD_KL (0) or REVERSE_KL (1)")
     loss = torch.empty((B, K), dtype=torch.float32, device=dev)
     if out_grad is not None:
-        _require(out_grad, "out_grad", draft_logits.dtype, (B, K, V), dev)
+        _fit(out_grad, "out_grad", draft_logits.dtype, (B, K, V), dev)
     elif need_grad:
         out_grad = torch.empty((B, K, V), dtype=draft_logits.dtype, device=dev)
-    st = load().specv_distill(
+    st = _entry("specv_distill")(
         target_logits.data_ptr(), draft_logits.data_ptr(),
         None if weight is None else weight.data_ptr(), B, K, V, tsb, tsk, dsb, dsk, code,
         int(kind), loss.data_ptr(), None if out_grad is None else out_grad.data_ptr(),
-        _stream_ptr(stream, dev))
-    _check(st, "specv_distill")
+        _stream(stream, dev))
+    if st:
+        _check(st, "specv_distill")
     return loss, out_grad
 
 
@@ -174,25 +205,38 @@ def clip_grads(grads, max_norm: float, out=None, stream=None) -> torch.Tensor:
     max_norm = float(max_norm)
     if not max_norm >= 0.0:
         raise ValueError("max_norm must be >= 0")
+    at, counts, codes = _table(grads, "gradient")
     dev = grads[0].device if grads else torch.device("cuda", torch.cuda.current_device())
-    table, seen = [], set()
-    for i, (g, o) in enumerate(zip(grads, out)):
-        if g.device != dev or dev.type != "cuda":
-            raise ValueError("gradients must be CUDA tensors of one device")
-        if not g.is_contiguous():
-            raise ValueError(f"gradient {i} must be contiguous")
-        code, n, p = _dtype_code(g), g.numel(), g.data_ptr()
-        if o is not g:
-            if o.dtype != g.dtype or o.numel() != n or o.device != dev or not o.is_contiguous():
-                raise ValueError(f"out[{i}] must match gradient {i} in type, size and device, "
-                                 "contiguous")
-        if n:
-            if p in seen:
-                raise ValueError(f"gradient {i} is listed twice")
-            seen.add(p)
-            table += (p, o.data_ptr(), n, code)
+    if out is grads:
+        to = at
+    else:
+        to, sizes, types = _table(out, "out")
+        if sizes != counts or types != codes or (out and out[0].device != dev):
+            raise ValueError("out must match the gradients in type, size and device")
+    live = [p for p, n in zip(at, counts) if n]
+    if len(set(live)) != len(live):
+        raise ValueError("a gradient is listed twice")
+    table = array("q", bytes(32 * len(grads)))
+    table[0::4], table[1::4] = array("q", at), array("q", to)
+    table[2::4], table[3::4] = array("q", counts), array("q", codes)
     norm = torch.empty((), dtype=torch.float32, device=dev)
-    st = load().specv_clip_grads((ctypes.c_int64 * len(table))(*table), len(table) // 4, max_norm,
-                                 norm.data_ptr(), _stream_ptr(stream, dev))
-    _check(st, "specv_clip_grads")
+    st = _entry("specv_clip_grads")(table.buffer_info()[0] if grads else None, len(grads), max_norm,
+                                    norm.data_ptr(), _stream(stream, dev))
+    if st:
+        _check(st, "specv_clip_grads")
     return norm
+
+
+def _table(tensors, name: str):
+    """(addresses, sizes, type codes) of contiguous CUDA tensors of one device."""
+    at = list(map(torch.Tensor.data_ptr, tensors))
+    devices = set(map(torch.Tensor.get_device, tensors))  # -1: not a CUDA device
+    if len(devices) > 1 or -1 in devices:
+        raise ValueError("gradients must be CUDA tensors of one device")
+    if not all(map(torch.Tensor.is_contiguous, tensors)):
+        raise ValueError(f"every {name} must be contiguous")
+    try:
+        codes = [_CODES[t] for t in map(attrgetter("dtype"), tensors)]
+    except KeyError as e:
+        raise TypeError(f"gradients must be float32 or bfloat16, got {e.args[0]}") from None
+    return at, list(map(torch.Tensor.numel, tensors)), codes
