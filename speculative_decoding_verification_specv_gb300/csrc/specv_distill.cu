@@ -379,6 +379,8 @@ __global__ void __launch_bounds__(kNT + 32, 4) distill_kernel(DistillArgs a, int
   if (w == 0.0f) {
     if (rank == 0 && tid == 0) a.out_loss[r] = 0.0f;
     zero_fill();
+    __syncwarp();
+    if (S > 1) cluster_sit_out();
     return;
   }
   if (tid == 0) {

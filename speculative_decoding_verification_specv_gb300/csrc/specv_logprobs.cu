@@ -23,6 +23,8 @@
 // pair's order makes equal values, a constant row for instance, select top_n
 // strips as well.  Rows that put more than kCand entries above the threshold take
 // a repeated search instead, whose result is the same.
+#include <algorithm>
+
 #include <cooperative_groups.h>
 
 #include "specv_block.cuh"
@@ -180,6 +182,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 1024 / NT)
   const int V = a.V, top_n = a.top_n;
   const int32_t x = a.tokens[r];
   if (x < 0 || x >= V) {  // no token (-1): the row is not read; an invalid one: NaN
+    if (CLUSTER) cluster_sit_out();
     if (rank != 0) return;
     const float fill = x == -1 ? 0.0f : quiet_nan();
     if (tid == 0) {
@@ -411,10 +414,14 @@ cudaError_t forward(const LogprobArgs &a, int sms, int S, cudaStream_t stream) {
   const int64_t vectors = (a.V + kVW - 1) / kVW;
   // Short rows: a warp per row, up to 8 vectors per lane.
   if (S == 0 && vectors <= 32 * 8) return launch_forward<T, 32, false>(a, 1, stream);
-  // CTAs per row: enough for two per SM, each with a batch of vectors at least.
+  // CTAs per row: as many as one wave of 4 CTAs per SM allows, up to 8, each with 1200
+  // vectors at least (a batch of the streaming loop is 1024).  Measured: 9 rows of
+  // 16032 vectors 6.6 us with S = 8, 7.8 with 16, 12.3 with 1; 185 rows of 12501 15.9
+  // with S = 2, 18.7 with 1, 21.1 with 4 (two waves); 77 rows of 1101 5.8 with S = 1,
+  // 6.5 with 2; 2304 rows of 32064 188 with S = 1, 214 with 2.
   if (S == 0) {
-    S = 1;
-    while (S < kMaxCluster && a.R * S < 2 * sms && vectors / (2 * S) >= 256 * kUnroll / 2) S *= 2;
+    const int64_t most = std::min<int64_t>(4 * sms / a.R, vectors / 1200);
+    S = (int)std::max<int64_t>(1, std::min<int64_t>(most, 8));
   }
   while (S > 1 && a.R * S > INT32_MAX) S /= 2;
   return S == 1 ? launch_forward<T, 256, false>(a, 1, stream)

@@ -52,6 +52,17 @@ __device__ __forceinline__ uint16_t narrow<uint16_t>(float x) {
 __device__ __forceinline__ float widen(float x) { return x; }
 __device__ __forceinline__ float widen(uint16_t x) { return bf16_bits_to_float(x); }
 
+// A CTA that has nothing to do for its row stays until the cluster's last barrier all
+// the same (it arrives like the others, once early and once at the end): CTAs of one
+// cluster that read different tokens or weights, because a caller writes them
+// meanwhile, then produce one wrong row and not a store into a CTA that has ended.
+__device__ __forceinline__ void cluster_sit_out() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+
 // ------------------------------------------------------- packed pairs of fp32
 // sm_103a adds, multiplies and fuses two fp32 values per instruction, each
 // rounded as its scalar form.
