@@ -11,7 +11,8 @@
 // up to 16 terms) and without further rounding beyond; every CTA writes its sum.  Every CTA of the
 // second launch adds those sums in the same order, so that all hold the same norm
 // (no atomics, one result), and scales its chunks, the last ones first: these the
-// first launch has left in L2.  The second launch begins while the first drains
+// first launch has left in L2, which the results, stored as streaming data, do not
+// push out.  The second launch begins while the first drains
 // (programmatic dependent launch).  Gradients of a call travel in the launches'
 // parameters, so nothing is copied to the device first.
 #include "specv_internal.h"
@@ -196,7 +197,7 @@ __device__ __forceinline__ void scale_chunk(const void *from, void *to, const Ch
   T *q = out + c.at + (int)threadIdx.x * VW;
   if (alike && c.whole) {
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u) *reinterpret_cast<uint4 *>(q + u * (kNT * VW)) = v[u];
+    for (int u = 0; u < kVecs; ++u) __stcs(reinterpret_cast<uint4 *>(q + u * (kNT * VW)), v[u]);
     return;
   }
 #pragma unroll

@@ -54,7 +54,7 @@ __device__ __forceinline__ void move_to(PairSums &x, float Mt, float Mq) {
 
 // ------------------------------------------------------------------ shared steps
 struct Merged {
-  float lt, lq;  // ln S of the target's and the draft's row
+  float lt, lq;  // log2 S of the target's and the draft's row
   float rt, rq;  // their references
   float kl;      // the divergence: NaN for a row with a NaN or +inf
   bool empty;    // a row masks every entry
@@ -97,11 +97,12 @@ __device__ __forceinline__ Merged merge_parts(const float4 *a, const float *t, i
   Merged m;
   const bool bad = !(y.st < INFINITY) || !(y.sq < INFINITY);
   m.empty = !bad && (y.st == 0.0f || y.sq == 0.0f);
-  m.lt = logf(y.st);
-  m.lq = logf(y.sq);
+  m.lt = lg2(y.st);
+  m.lq = lg2(y.sq);
   m.rt = y.rt;
   m.rq = y.rq;
-  const float kl = REVERSE ? y.t / y.sq - m.lq + m.lt : y.t / y.st - m.lt + m.lq;
+  const float mean = __fdividef(y.t, REVERSE ? y.sq : y.st);
+  const float kl = __fmaf_rn(REVERSE ? m.lt - m.lq : m.lq - m.lt, kLn2, mean);
   m.kl = bad ? quiet_nan() : kl < 0.0f ? 0.0f : kl;
   return m;
 }
@@ -159,11 +160,11 @@ struct GradTerms {
   __device__ __forceinline__ GradTerms(const Merged &m, float weight) {
     bad = m.kl != m.kl;
     const float wg = bad ? quiet_nan() : weight;
-    const float cc = m.kl == INFINITY ? quiet_nan() : m.lt - m.lq - m.kl;
+    const float cc = m.kl == INFINITY ? quiet_nan() : (m.lt - m.lq) * kLn2 - m.kl;
     rt = pack2(-m.rt, -m.rt);
     rq = pack2(-m.rq, -m.rq);
-    lt = pack2(-m.lt * kLog2e, -m.lt * kLog2e);
-    lq = pack2(-m.lq * kLog2e, -m.lq * kLog2e);
+    lt = pack2(-m.lt, -m.lt);
+    lq = pack2(-m.lq, -m.lq);
     w = pack2(wg, wg);
     c = pack2(cc, cc);
   }
@@ -376,13 +377,6 @@ __global__ void __launch_bounds__(kNT + 32, 4) distill_kernel(DistillArgs a, int
     if (out == nullptr || warp == kNW) return;
     for (int k = lo + tid; k < hi; k += kNT) store_pack<T>(out, grid, k, make_uint4(0, 0, 0, 0));
   };
-  if (w == 0.0f) {
-    if (rank == 0 && tid == 0) a.out_loss[r] = 0.0f;
-    zero_fill();
-    __syncwarp();
-    if (S > 1) cluster_sit_out();
-    return;
-  }
   if (tid == 0) {
     sh.lost = 0;
     for (int b = 0; b < kBuffers; ++b) {
@@ -393,6 +387,12 @@ __global__ void __launch_bounds__(kNT + 32, 4) distill_kernel(DistillArgs a, int
   }
   if (S > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   __syncthreads();
+  if (w == 0.0f) {
+    if (rank == 0 && tid == 0) a.out_loss[r] = 0.0f;
+    zero_fill();
+    if (S > 1) cluster_sit_out();
+    return;
+  }
 
   const GridRow<T, SHIFTED> rt(zt, grid), rq(zq, grid);
   auto buffer = [&](int c, int which) {
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(kNT + 32, 4) distill_kernel(DistillArgs a, int
     if (inner) {
       uint4 *to = reinterpret_cast<uint4 *>(out + ((int64_t)k0 * Elem<T>::kPerVec - grid.mis));
 #pragma unroll
-      for (int j = 0; j < kUnroll; ++j) to[j * kNT] = xq.v[j];
+      for (int j = 0; j < kUnroll; ++j) __stcs(to + j * kNT, xq.v[j]);
     } else {
 #pragma unroll
       for (int j = 0; j < kUnroll; ++j)

@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 1024 / NT)
   const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int V = a.V, top_n = a.top_n;
   const int32_t x = a.tokens[r];
+  if (CLUSTER) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   if (x < 0 || x >= V) {  // no token (-1): the row is not read; an invalid one: NaN
     if (CLUSTER) cluster_sit_out();
     if (rank != 0) return;
@@ -196,7 +197,6 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 1024 / NT)
     }
     return;
   }
-  if (CLUSTER) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const T *first = static_cast<const T *>(a.logits) + row_offset(r, a.N, a.stride_b, a.stride_n);
   const RowVectors<T> row(first, V);
   const int per = (row.count + S - 1) / S;
@@ -324,20 +324,26 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 1024 / NT)
 // ------------------------------------------------------------------ the gradient
 //   dz_v = g (1[v = x] - p_v) - h p_v (ln p_v + H)
 // from the statistics of the forward pass: each entry is read and its gradient
-// written once.  A warp takes kGradUnroll packs per lane of one row, on the grid of
+// written once.  A warp takes some packs per lane of one row, on the grid of
 // the output's row.
 constexpr int kGradNT = 256;
-constexpr int kGradUnroll = 4;
-constexpr int kGradUnit = 32 * kGradUnroll;  // packs of a warp's share
+// Packs per lane: 8 in flight for aligned rows; rows to be joined keep 4 (their
+// registers).  2048 rows of 128256 bf16 entries: 144 us with 8, 151 with 4, 162 with 2;
+// 2349 rows of 14957 in a padded buffer: 25 us with 4, 30 with 8.
+template <bool SHIFTED>
+constexpr int kGradUnroll = SHIFTED ? 4 : 8;
+template <bool SHIFTED>
+constexpr int kGradUnit = 32 * kGradUnroll<SHIFTED>;  // packs of a warp's share
 
 template <typename T, bool SHIFTED>
 __global__ void __launch_bounds__(kGradNT) logprobs_grad_kernel(LogprobGradArgs a, uint32_t units) {
   constexpr int VW = Elem<T>::kPerVec;
+  constexpr int U = kGradUnroll<SHIFTED>, kUnit = kGradUnit<SHIFTED>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint64_t unit = (uint64_t)blockIdx.x * (kGradNT / 32) + warp;  // share `unit % units` of row
   const int64_t r = unit >> 32 == 0 ? (uint32_t)unit / units : unit / units;
   if (r >= a.R) return;
-  const int k0 = (int)(unit - (uint64_t)r * units) * kGradUnit;
+  const int k0 = (int)(unit - (uint64_t)r * units) * kUnit;
   const T *row = static_cast<const T *>(a.logits) + row_offset(r, a.N, a.stride_b, a.stride_n);
   T *out = static_cast<T *>(a.out) + r * (int64_t)a.V;
   const Grid<T> grid(out, a.V);
@@ -347,13 +353,13 @@ __global__ void __launch_bounds__(kGradNT) logprobs_grad_kernel(LogprobGradArgs 
   const float h = a.grad_entropy != nullptr ? a.grad_entropy[r] : 0.0f;
   const bool bad = x < -1 || x >= a.V;
   const bool zero = x == -1 || (!bad && st.x == -INFINITY);
-  PackTile<T, SHIFTED, kGradUnroll> z;
+  PackTile<T, SHIFTED, U> z;
   if (zero || bad) {
     const float fill = zero ? 0.0f : quiet_nan();
 #pragma unroll
     for (int i = 0; i < z.kPairs; ++i) z.put(i, fill, fill);
 #pragma unroll
-    for (int j = 0; j < kGradUnroll; ++j) {
+    for (int j = 0; j < U; ++j) {
       const int k = k0 + 32 * j + lane;
       if (k < grid.count) store_pack<T>(out, grid, k, z.v[j]);
     }
@@ -363,7 +369,7 @@ __global__ void __launch_bounds__(kGradNT) logprobs_grad_kernel(LogprobGradArgs 
   z.load(from, grid, k0, grid.count);
   // the lane that holds the token's entry
   const int64_t kx = ((int64_t)x + grid.mis) / VW;
-  const bool mine = kx >= k0 && kx < k0 + kGradUnit && ((int)(kx - k0) & 31) == lane;
+  const bool mine = kx >= k0 && kx < k0 + kUnit && ((int)(kx - k0) & 31) == lane;
   float zx = 0.0f;
   if (mine) zx = widen(*reinterpret_cast<const volatile T *>(row + x));
   z.join(from);
@@ -382,7 +388,7 @@ __global__ void __launch_bounds__(kGradNT) logprobs_grad_kernel(LogprobGradArgs 
     z.put(i, d0, d1);
   }
 #pragma unroll
-  for (int j = 0; j < kGradUnroll; ++j) {
+  for (int j = 0; j < U; ++j) {
     const int k = k0 + 32 * j + lane;
     if (k < grid.count) store_pack<T>(out, grid, k, z.v[j]);
   }
@@ -449,7 +455,7 @@ static cudaError_t launch_grad(const LogprobGradArgs &a, cudaStream_t stream) {
   constexpr int VW = Elem<T>::kPerVec;
   // shares of a row, wherever it begins
   const int64_t packs = ((int64_t)a.V + (SHIFTED ? 2 : 1) * (VW - 1)) / VW;
-  const int64_t units = (packs + kGradUnit - 1) / kGradUnit;
+  const int64_t units = (packs + kGradUnit<SHIFTED> - 1) / kGradUnit<SHIFTED>;
   const int64_t ctas = (a.R * units + kGradNT / 32 - 1) / (kGradNT / 32);
   if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
   logprobs_grad_kernel<T, SHIFTED><<<(unsigned)ctas, kGradNT, 0, stream>>>(a, (uint32_t)units);
