@@ -35,6 +35,13 @@ bool view_ok(int64_t B, int32_t N, int32_t V, int64_t sb, int64_t sn) {
   return sb <= kLimit / 4 / B && sn <= kLimit / 4 / N;
 }
 
+// Past the last element of such a view.
+const void *view_end(const void *p, int64_t B, int32_t N, int32_t V, int64_t sb, int64_t sn,
+                     int64_t dtype) {
+  return static_cast<const char *>(p) +
+         ((B - 1) * sb + (N - 1) * sn + V) * (dtype == SPECV_BF16 ? 2 : 4);
+}
+
 bool dtype_ok(int64_t dtype) { return dtype == SPECV_F32 || dtype == SPECV_BF16; }
 
 bool misaligned(const void *p, int64_t dtype) {
@@ -105,6 +112,7 @@ specv_status specv_token_logprobs(const void *logits, const int32_t *tokens, int
   if (ready != SPECV_OK) return (specv_status)ready;
   specv::LogprobArgs a;
   a.logits = logits;
+  a.logits_end = view_end(logits, B, N, V, stride_b, stride_n, dtype);
   a.tokens = tokens;
   a.R = B * N;
   a.N = N;
@@ -138,6 +146,7 @@ specv_status specv_token_logprobs_backward(const void *logits, const int32_t *to
   if (ready != SPECV_OK) return (specv_status)ready;
   specv::LogprobGradArgs a;
   a.logits = logits;
+  a.logits_end = view_end(logits, B, N, V, stride_b, stride_n, dtype);
   a.tokens = tokens;
   a.stats = reinterpret_cast<const float2 *>(stats);
   a.entropy = entropy;
@@ -173,6 +182,8 @@ specv_status specv_distill(const void *target_logits, const void *draft_logits,
   specv::DistillArgs a;
   a.target = target_logits;
   a.draft = draft_logits;
+  a.target_end = view_end(target_logits, B, K, V, target_stride_b, target_stride_k, dtype);
+  a.draft_end = view_end(draft_logits, B, K, V, draft_stride_b, draft_stride_k, dtype);
   a.weight = weight;
   a.B = B;
   a.K = K;

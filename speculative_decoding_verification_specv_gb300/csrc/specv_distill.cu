@@ -71,6 +71,22 @@ __device__ __forceinline__ void merge_lanes(PairSums &y) {
   }
 }
 
+// What follows from a pair's sums.
+template <bool REVERSE>
+__device__ __forceinline__ Merged merged(const PairSums &y) {
+  Merged m;
+  const bool bad = !(y.st < INFINITY) || !(y.sq < INFINITY);
+  m.empty = !bad && (y.st == 0.0f || y.sq == 0.0f);
+  m.lt = lg2(y.st);
+  m.lq = lg2(y.sq);
+  m.rt = y.rt;
+  m.rq = y.rq;
+  const float mean = __fdividef(y.t, REVERSE ? y.sq : y.st);
+  const float kl = __fmaf_rn(REVERSE ? m.lt - m.lq : m.lq - m.lt, kLn2, mean);
+  m.kl = bad ? quiet_nan() : kl < 0.0f ? 0.0f : kl;
+  return m;
+}
+
 // The partials of `parts` warps (a: rt, st, rq, sq), merged by a warp; every lane
 // returns the same.
 template <bool REVERSE>
@@ -94,17 +110,7 @@ __device__ __forceinline__ Merged merge_parts(const float4 *a, const float *t, i
     y.t += z.t;
   }
   merge_lanes<REVERSE>(y);
-  Merged m;
-  const bool bad = !(y.st < INFINITY) || !(y.sq < INFINITY);
-  m.empty = !bad && (y.st == 0.0f || y.sq == 0.0f);
-  m.lt = lg2(y.st);
-  m.lq = lg2(y.sq);
-  m.rt = y.rt;
-  m.rq = y.rq;
-  const float mean = __fdividef(y.t, REVERSE ? y.sq : y.st);
-  const float kl = __fmaf_rn(REVERSE ? m.lt - m.lq : m.lq - m.lt, kLn2, mean);
-  m.kl = bad ? quiet_nan() : kl < 0.0f ? 0.0f : kl;
-  return m;
+  return merged<REVERSE>(y);
 }
 
 // t += e d where e > 0, else nothing, whatever d is.
@@ -196,17 +202,15 @@ __device__ __forceinline__ void gradient(const GradTerms &g, const TileT &xt, Ti
 }
 
 // ------------------------------------------------------------------- short rows
-// One CTA of 64 threads per pair, at most two register tiles of it.
-constexpr int kSmallNT = 64;
-constexpr int kPackUnroll = 2;  // packs per lane of a tile
+// A warp per pair, which it holds in registers: U packs of each row per lane.
+constexpr int kShortNT = 128;
+constexpr int kShortPacks = 8;  // U at most: pairs of 2048 bf16 or 1024 fp32 entries
 
-template <typename T, bool SHIFTED, bool REVERSE>
-__global__ void __launch_bounds__(kSmallNT) distill_short_kernel(DistillArgs a) {
-  constexpr int kNW = kSmallNT / 32;
-  __shared__ float4 part_a[kNW];
-  __shared__ float part_t[kNW];
-  const int64_t r = blockIdx.x;
-  const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
+template <typename T, bool SHIFTED, bool REVERSE, int U>
+__global__ void __launch_bounds__(kShortNT) distill_short_kernel(DistillArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t r = (int64_t)blockIdx.x * (kShortNT / 32) + (threadIdx.x >> 5);
+  if (r >= a.B * a.K) return;
   const T *zt =
       static_cast<const T *>(a.target) + row_offset(r, a.K, a.target_stride_b, a.target_stride_k);
   const T *zq =
@@ -214,54 +218,43 @@ __global__ void __launch_bounds__(kSmallNT) distill_short_kernel(DistillArgs a) 
   T *out = a.out_grad == nullptr ? nullptr : static_cast<T *>(a.out_grad) + r * (int64_t)a.V;
   const Grid<T> grid(out != nullptr ? static_cast<const void *>(out) : zq, a.V);
   const float w = a.weight == nullptr ? 1.0f : a.weight[r];
-  auto zero_fill = [&]() {
+  PackTile<T, SHIFTED, U> xt, xq;
+  auto store = [&]() {
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int k = 32 * j + lane;
+      if (k < grid.count) store_pack<T>(out, grid, k, xq.v[j]);
+    }
+  };
+  auto zero = [&]() {
+    if (lane == 0) a.out_loss[r] = 0.0f;
     if (out == nullptr) return;
-    for (int k = tid; k < grid.count; k += kSmallNT)
-      store_pack<T>(out, grid, k, make_uint4(0, 0, 0, 0));
+#pragma unroll
+    for (int i = 0; i < xq.kPairs; ++i) xq.put(i, 0.0f, 0.0f);
+    store();
   };
   if (w == 0.0f) {
-    if (tid == 0) a.out_loss[r] = 0.0f;
-    zero_fill();
+    zero();
     return;
   }
-  const GridRow<T, SHIFTED> rt(zt, grid), rq(zq, grid);
-  constexpr int kTile = kPackUnroll * kSmallNT;
-  PackTile<T, SHIFTED, kPackUnroll> xt[2], xq[2];
+  const GridRow<T, SHIFTED> rt(zt, grid, Span{a.target, a.target_end}),
+      rq(zq, grid, Span{a.draft, a.draft_end});
+  xt.load(rt, grid, 0, grid.count);
+  xq.load(rq, grid, 0, grid.count);
+  xt.join(rt, grid, 0, grid.count);
+  xq.join(rq, grid, 0, grid.count);
   PairSums x;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    xt[i].load(rt, grid, i * kTile + warp * 32 * kPackUnroll, grid.count);
-    xq[i].load(rq, grid, i * kTile + warp * 32 * kPackUnroll, grid.count);
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    xt[i].join(rt);
-    xq[i].join(rq);
-    fold_pair<T, REVERSE>(x, xt[i], xq[i]);
-  }
+  fold_pair<T, REVERSE>(x, xt, xq);
   merge_lanes<REVERSE>(x);
-  if (lane == 0) {
-    part_a[warp] = make_float4(x.rt, x.st, x.rq, x.sq);
-    part_t[warp] = x.t;
-  }
-  __syncthreads();
-  const Merged m = merge_parts<REVERSE>(part_a, part_t, kNW);
-  if (tid == 0) a.out_loss[r] = m.empty ? 0.0f : w * m.kl;
-  if (out == nullptr) return;
+  const Merged m = merged<REVERSE>(x);
   if (m.empty) {
-    zero_fill();
+    zero();
     return;
   }
-  const GradTerms g(m, w);
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    gradient<T, REVERSE>(g, xt[i], xq[i]);
-#pragma unroll
-    for (int j = 0; j < kPackUnroll; ++j) {
-      const int k = i * kTile + (warp * kPackUnroll + j) * 32 + lane;
-      if (k < grid.count) store_pack<T>(out, grid, k, xq[i].v[j]);
-    }
-  }
+  if (lane == 0) a.out_loss[r] = w * m.kl;
+  if (out == nullptr) return;
+  gradient<T, REVERSE>(GradTerms(m, w), xt, xq);
+  store();
 }
 
 // -------------------------------------------------------------------- long rows
@@ -305,8 +298,9 @@ struct ChunkTile {
       if (k >= r.lo && k < r.hi) {
         v[j] = p[j * kNT];
         if (SHIFTED && r.shift != 0) v[j] = shifted<T>(v[j], p[j * kNT + 1], r.shift);
+        if (SHIFTED && !grid.full(k)) mask_outside<T>(v[j], (int64_t)k * VW - grid.mis, grid.V);
       } else if (SHIFTED) {
-        v[j] = PackTile<T, SHIFTED, 1>::load_entries(r.row, (int64_t)k * VW - grid.mis, grid.V);
+        v[j] = load_entries<T>(r.row, (int64_t)k * VW - grid.mis, grid.V);
       }
     }
   }
@@ -394,7 +388,8 @@ __global__ void __launch_bounds__(kNT + 32, 4) distill_kernel(DistillArgs a, int
     return;
   }
 
-  const GridRow<T, SHIFTED> rt(zt, grid), rq(zq, grid);
+  const GridRow<T, SHIFTED> rt(zt, grid, Span{a.target, a.target_end}),
+      rq(zq, grid, Span{a.draft, a.draft_end});
   auto buffer = [&](int c, int which) {
     return reinterpret_cast<uint4 *>(chunks + ((c % kBuffers) * 2 + which) * kChunkBytes);
   };
@@ -541,9 +536,15 @@ cudaError_t plan(const DistillArgs &a, int S, cudaStream_t stream) {
   constexpr int kVW = Elem<T>::kPerVec;
   // packs of a row, wherever it begins
   const int64_t packs = ((int64_t)a.V + (SHIFTED ? 2 : 1) * (kVW - 1)) / kVW;
-  if (S == 0 && packs <= 2 * kSmallNT * kPackUnroll) {
-    distill_short_kernel<T, SHIFTED, REVERSE>
-        <<<(unsigned)(a.B * a.K), kSmallNT, 0, stream>>>(a);
+  if (S == 0 && packs <= 32 * kShortPacks) {
+    const int64_t ctas = (a.B * a.K + kShortNT / 32 - 1) / (kShortNT / 32);
+    if (packs <= 32 * 2)
+      distill_short_kernel<T, SHIFTED, REVERSE, 2><<<(unsigned)ctas, kShortNT, 0, stream>>>(a);
+    else if (packs <= 32 * 4)
+      distill_short_kernel<T, SHIFTED, REVERSE, 4><<<(unsigned)ctas, kShortNT, 0, stream>>>(a);
+    else
+      distill_short_kernel<T, SHIFTED, REVERSE, kShortPacks>
+          <<<(unsigned)ctas, kShortNT, 0, stream>>>(a);
     return cudaGetLastError();
   }
   if (S == 0) {

@@ -271,6 +271,7 @@ cudaError_t tile_launch(const TileArgs &a, int dtype_bf16, int mode, int64_t gri
 // Arguments of the log-probability kernel: rows (b, n) of a [B][N][V] view.
 struct LogprobArgs {
   const void *logits;        // element (b, n, v) at b * stride_b + n * stride_n + v
+  const void *logits_end;    // past the view's last element
   const int32_t *tokens;     // [R]: -1 = no token, the row is not read
   int64_t R;                 // B * N rows
   int N;
@@ -292,6 +293,7 @@ cudaError_t logprobs_launch(const LogprobArgs &a, int dtype_bf16, int sms, int S
 // Arguments of the log-probability gradient kernel.
 struct LogprobGradArgs {
   const void *logits;
+  const void *logits_end;    // past the view's last element
   const int32_t *tokens;     // [R]
   const float2 *stats;       // [R]
   const float *entropy;      // [R]
@@ -309,6 +311,8 @@ cudaError_t logprobs_grad_launch(const LogprobGradArgs &a, int dtype_bf16, cudaS
 struct DistillArgs {
   const void *target;        // row (b, i) at b * target_stride_b + i * target_stride_k
   const void *draft;         // row (b, i) at b * draft_stride_b + i * draft_stride_k
+  const void *target_end;    // past the views' last elements
+  const void *draft_end;
   const float *weight;       // [B][K], or null: ones
   int64_t B;
   int K;

@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 1024 / NT)
     return;
   }
   const T *first = static_cast<const T *>(a.logits) + row_offset(r, a.N, a.stride_b, a.stride_n);
-  const RowVectors<T> row(first, V);
+  const RowVectors<T> row(first, V, Span{a.logits, a.logits_end});
   const int per = (row.count + S - 1) / S;
   const int lo = min(row.count, rank * per), hi = min(row.count, lo + per);
   const float zx = rank == 0 && tid == 0 ? Elem<T>::load(first + x) : 0.0f;
@@ -365,14 +365,14 @@ __global__ void __launch_bounds__(kGradNT) logprobs_grad_kernel(LogprobGradArgs 
     }
     return;
   }
-  const GridRow<T, SHIFTED> from(row, grid);
+  const GridRow<T, SHIFTED> from(row, grid, Span{a.logits, a.logits_end});
   z.load(from, grid, k0, grid.count);
   // the lane that holds the token's entry
   const int64_t kx = ((int64_t)x + grid.mis) / VW;
   const bool mine = kx >= k0 && kx < k0 + kUnit && ((int)(kx - k0) & 31) == lane;
   float zx = 0.0f;
   if (mine) zx = widen(*reinterpret_cast<const volatile T *>(row + x));
-  z.join(from);
+  z.join(from, grid, k0, grid.count);
 
   const uint64_t m2 = pack2(-st.x, -st.x), l2 = pack2(-st.y, -st.y), scale = pack2(kLog2e, kLog2e);
   const float c = -__fmaf_rn(h, H, g);  // out = p (c - h ln p)

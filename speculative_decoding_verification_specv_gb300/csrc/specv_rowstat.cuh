@@ -91,20 +91,61 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 }
 
 // --------------------------------------------------------------- rows as vectors
-// A row seen as 16-byte vectors of the aligned memory that holds it: vector k
-// covers entries [k VW - mis, (k + 1) VW - mis).  Vectors [full_lo, full_hi) lie
-// within the row; the others (the first of a row off a 16-byte boundary, the last
-// of a ragged one) are read entry by entry, and what is not the row's is -inf.
+// Replaces the entries of a vector that lie outside [0, V) by -inf; its first entry
+// has index `first`.
+template <typename T>
+__device__ __forceinline__ void mask_outside(uint4 &v, int64_t first, int V) {
+#pragma unroll
+  for (int e = 0; e < Elem<T>::kPerVec; ++e)
+    if (first + e < 0 || first + e >= V) Elem<T>::put_bits(v, e, Elem<T>::kNegInfBits);
+}
+
+// Entries [first, first + VW) of a row, one by one: what lies outside the row is -inf.
+template <typename T>
+__device__ __noinline__ uint4 load_entries(const T *row, int64_t first, int V) {
+  constexpr uint32_t none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+  uint4 x = make_uint4(none, none, none, none);
+#pragma unroll
+  for (int e = 0; e < Elem<T>::kPerVec; ++e) {
+    const int64_t c = first + e;
+    if (c >= 0 && c < V) {
+      uint32_t bits;
+      if constexpr (sizeof(T) == 2) {
+        uint16_t h;
+        asm volatile("ld.global.u16 %0, [%1];" : "=h"(h) : "l"(row + c));
+        bits = h;
+      } else {
+        asm volatile("ld.global.u32 %0, [%1];" : "=r"(bits) : "l"(row + c));
+      }
+      Elem<T>::put_bits(x, e, bits);
+    }
+  }
+  return x;
+}
+
+// The memory that a view of rows spans, from its first entry to past its last.  Any
+// whole 16-byte vector within it may be read: one that straddles a row's end brings
+// entries of a neighbouring row or of the gap between rows, which are replaced by
+// -inf.  Only the span's own ends are read entry by entry.
+struct Span {
+  const void *lo, *hi;
+};
+
+// A row seen as 16-byte vectors of the aligned memory that holds it: vector k covers
+// entries [k VW - mis, (k + 1) VW - mis).  Vectors [full_lo, full_hi) lie within the
+// row; vectors [lo, hi) within the span.
 template <typename T>
 struct RowVectors {
+  const T *row;
   const char *base;  // 16-byte aligned, at or before the row's first entry
   int mis;           // entries between base and the row's first one
   int V;
   int count;         // vectors that hold entries of the row
-  int full_lo, full_hi;
+  int full_lo, full_hi, lo, hi;
 
-  __device__ __forceinline__ RowVectors(const T *row, int V_) {
+  __device__ __forceinline__ RowVectors(const T *row_, int V_, const Span &span) {
     constexpr int VW = Elem<T>::kPerVec;
+    row = row_;
     const uint64_t at = reinterpret_cast<uint64_t>(row);
     mis = (int)(at % 16) / (int)sizeof(T);
     base = reinterpret_cast<const char *>(at - at % 16);
@@ -112,8 +153,9 @@ struct RowVectors {
     count = (int)(((int64_t)V + mis + VW - 1) / VW);
     full_lo = mis != 0 ? 1 : 0;
     full_hi = (int)(((int64_t)V + mis) / VW);
+    lo = base >= span.lo ? 0 : 1;
+    hi = base + (int64_t)count * 16 <= span.hi ? count : full_hi;
   }
-  __device__ __forceinline__ bool full(int k) const { return k >= full_lo && k < full_hi; }
   // the entry's index in the row (outside [0, V) for what an edge vector pads)
   __device__ __forceinline__ int64_t index(int k, int e) const {
     return (int64_t)k * Elem<T>::kPerVec + e - mis;
@@ -121,18 +163,12 @@ struct RowVectors {
   __device__ __forceinline__ uint4 load_full(int k) const {
     return ld_stream16(base + (int64_t)k * 16);
   }
-  __device__ __noinline__ uint4 load_edge(int k) const {
-    constexpr uint32_t none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
-    uint4 v = make_uint4(none, none, none, none);
-    const T *p = reinterpret_cast<const T *>(base + (int64_t)k * 16);
-#pragma unroll
-    for (int e = 0; e < Elem<T>::kPerVec; ++e) {
-      const int64_t c = index(k, e);
-      if (c >= 0 && c < V) Elem<T>::put_bits(v, e, Elem<T>::load_bits(p + e));
-    }
+  __device__ __forceinline__ uint4 load(int k) const {
+    if (k < lo || k >= hi) return load_entries<T>(row, index(k, 0), V);
+    uint4 v = load_full(k);
+    if (k < full_lo || k >= full_hi) mask_outside<T>(v, index(k, 0), V);
     return v;
   }
-  __device__ __forceinline__ uint4 load(int k) const { return full(k) ? load_full(k) : load_edge(k); }
 };
 
 // Entries 2 i and 2 i + 1 of a vector, widened to a packed pair.
@@ -253,10 +289,10 @@ struct GridRow {
   const T *row;
   const char *base;   // the vector that holds the grid's pack 0 (or its start)
   int shift;          // 0..VW-1
-  int lo, hi;         // packs whose vectors lie within the row
-  int first, last;    // the row's whole vectors, counted from base
+  int first, last;    // the vectors of the row, counted from base, that may be read
+  int lo, hi;         // packs whose vectors may be read
 
-  __device__ __forceinline__ GridRow(const T *row_, const Grid<T> &grid) {
+  __device__ __forceinline__ GridRow(const T *row_, const Grid<T> &grid, const Span &span) {
     constexpr int VW = Elem<T>::kPerVec;
     row = row_;
     const uint64_t at = reinterpret_cast<uint64_t>(row);
@@ -272,9 +308,13 @@ struct GridRow {
     const int back = d < 0 ? 1 : 0;
     shift = d + back * VW;
     base = reinterpret_cast<const char *>(at - at % 16) - back * 16;
-    // pack k is joined from vectors k - back and, with a shift, k - back + 1
-    lo = first = back + (mis != 0 ? 1 : 0);
-    last = (int)(((int64_t)grid.V + mis) / VW) + back;
+    // pack k is joined from vectors k and, with a shift, k + 1; of those up to the one
+    // past the last pack, the ones within the span
+    const int64_t before = static_cast<const char *>(span.lo) - base;
+    const int64_t room = (static_cast<const char *>(span.hi) - base) / 16;
+    first = before > 0 ? (int)((before + 15) / 16) : 0;
+    last = room < grid.count + 1 ? (int)room : grid.count + 1;
+    lo = first;
     hi = last - (shift != 0 ? 1 : 0);
   }
 };
@@ -318,7 +358,6 @@ template <typename T, bool SHIFTED, int U>
 struct PackTile {
   static constexpr int kPairs = U * Elem<T>::kPerVec / 2;  // packed pairs of entries
   uint4 v[U + (SHIFTED ? 1 : 0)];
-  bool joined;  // the packs are whole (else v holds vectors still to be joined)
 
   __device__ __forceinline__ static uint4 load16(const char *p) {
     uint4 x;
@@ -331,72 +370,64 @@ struct PackTile {
     constexpr uint32_t n = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
     return make_uint4(n, n, n, n);
   }
-  // pack k entry by entry: what lies outside the row is -inf
-  __device__ __noinline__ static uint4 load_entries(const T *row, int64_t first, int V) {
-    uint4 x = none();
-#pragma unroll
-    for (int e = 0; e < Elem<T>::kPerVec; ++e) {
-      const int64_t c = first + e;
-      if (c >= 0 && c < V) {
-        uint32_t bits;
-        if constexpr (sizeof(T) == 2) {
-          uint16_t h;
-          asm volatile("ld.global.u16 %0, [%1];" : "=h"(h) : "l"(row + c));
-          bits = h;
-        } else {
-          asm volatile("ld.global.u32 %0, [%1];" : "=r"(bits) : "l"(row + c));
-        }
-        Elem<T>::put_bits(x, e, bits);
-      }
-    }
-    return x;
+  // whether every pack of the share is whole, and its vectors may be read
+  __device__ __forceinline__ static bool plain(const GridRow<T, SHIFTED> &r, const Grid<T> &grid,
+                                               int k0, int end) {
+    return k0 >= max(r.lo, grid.full_lo) && k0 + 32 * U <= min(min(r.hi, grid.full_hi), end);
   }
 
-  // The packs k0 + 32 j + lane below `end`; the others are -inf.
+  // The vectors of packs k0 + 32 j + lane, on their way.
   __device__ __forceinline__ void load(const GridRow<T, SHIFTED> &r, const Grid<T> &grid, int k0,
                                        int end) {
-    constexpr int VW = Elem<T>::kPerVec;
     const int lane = threadIdx.x & 31;
-    if (k0 >= r.lo && k0 + 32 * U <= min(r.hi, end)) {
-      const char *p = r.base + ((int64_t)k0 + lane) * 16;
+    const char *p = r.base + ((int64_t)k0 + lane) * 16;
+    if (plain(r, grid, k0, end)) {
 #pragma unroll
       for (int j = 0; j < U; ++j) v[j] = load16(p + j * 512);
-      if (SHIFTED) {
-        joined = r.shift == 0;
-        // lane 31's second vector of the last pack, fetched by lane 0
-        if (!joined && lane == 0) v[U] = load16(p + U * 512);
-      }
+      // lane 31's second vector of the last pack, fetched by lane 0
+      if (SHIFTED && r.shift != 0 && lane == 0) v[U] = load16(p + U * 512);
       return;
     }
-    joined = true;
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
+    for (int j = 0; j < U + (SHIFTED ? 1 : 0); ++j) {
       const int k = k0 + 32 * j + lane;
       v[j] = none();
-      if (k < end) {
-        if (k >= r.lo && k < r.hi && r.shift == 0)
-          v[j] = load16(r.base + (int64_t)k * 16);
-        else
-          v[j] = load_entries(r.row, (int64_t)k * VW - grid.mis, grid.V);
-      }
+      if (k >= r.first && k < min(r.last, end + (SHIFTED ? 1 : 0)) && (j < U || lane == 0))
+        v[j] = load16(p + j * 512);
     }
   }
 
-  // Joins the packs from their vectors (every lane of the warp).
-  __device__ __forceinline__ void join(const GridRow<T, SHIFTED> &r) {
-    if (!SHIFTED || joined) return;
-    const int lane = threadIdx.x & 31;
+  // Joins the packs from their vectors (every lane of the warp); what lies outside the
+  // row or at `end` and after becomes -inf.
+  __device__ __forceinline__ void join(const GridRow<T, SHIFTED> &r, const Grid<T> &grid, int k0,
+                                       int end) {
+    if constexpr (SHIFTED) {
+      const int lane = threadIdx.x & 31;
+      if (r.shift != 0) {
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
-      const uint4 &n = v[j + 1];
-      uint4 next;  // the next lane's vector; lane 31's is the next pack's first
-      next.x = __shfl_sync(0xffffffffu, lane == 0 ? n.x : v[j].x, (lane + 1) & 31);
-      next.y = __shfl_sync(0xffffffffu, lane == 0 ? n.y : v[j].y, (lane + 1) & 31);
-      next.z = __shfl_sync(0xffffffffu, lane == 0 ? n.z : v[j].z, (lane + 1) & 31);
-      next.w = __shfl_sync(0xffffffffu, lane == 0 ? n.w : v[j].w, (lane + 1) & 31);
-      v[j] = shifted<T>(v[j], next, r.shift);
+        for (int j = 0; j < U; ++j) {
+          const uint4 &n = v[j + 1];
+          uint4 next;  // the next lane's vector; lane 31's is the next pack's first
+          next.x = __shfl_sync(0xffffffffu, lane == 0 ? n.x : v[j].x, (lane + 1) & 31);
+          next.y = __shfl_sync(0xffffffffu, lane == 0 ? n.y : v[j].y, (lane + 1) & 31);
+          next.z = __shfl_sync(0xffffffffu, lane == 0 ? n.z : v[j].z, (lane + 1) & 31);
+          next.w = __shfl_sync(0xffffffffu, lane == 0 ? n.w : v[j].w, (lane + 1) & 31);
+          v[j] = shifted<T>(v[j], next, r.shift);
+        }
+      }
+      if (plain(r, grid, k0, end)) return;
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const int k = k0 + 32 * j + lane;
+        const int64_t c = (int64_t)k * Elem<T>::kPerVec - grid.mis;
+        if (k >= end)
+          v[j] = none();
+        else if (k < r.lo || k >= r.hi)
+          v[j] = load_entries<T>(r.row, c, grid.V);
+        else if (!grid.full(k))
+          mask_outside<T>(v[j], c, grid.V);
+      }
     }
-    joined = true;
   }
 
   __device__ __forceinline__ uint64_t pair(int i) const {
