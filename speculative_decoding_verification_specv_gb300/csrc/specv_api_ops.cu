@@ -194,7 +194,7 @@ specv_status specv_distill(const void *target_logits, const void *draft_logits,
   a.draft_stride_k = draft_stride_k;
   a.out_loss = out_loss;
   a.out_grad = out_grad;
-  return status_of(specv::distill_launch(a, dtype == SPECV_BF16, kind == SPECV_REVERSE_KL,
+  return status_of(specv::distill_launch(a, dtype == SPECV_BF16, kind == SPECV_REVERSE_KL, sms,
                                          specv::cluster_override(), static_cast<cudaStream_t>(stream)));
 }
 

@@ -15,6 +15,8 @@
 // cluster's registers is read once; of a longer one all but the last tile is read
 // again, from L2.  One cluster barrier lies between the passes: every warp sends
 // its partial sums to every CTA of the cluster, and each warp merges all of them.
+#include <algorithm>
+
 #include <cooperative_groups.h>
 
 #include "specv_block.cuh"
@@ -207,7 +209,7 @@ constexpr int kShortNT = 128;
 constexpr int kShortPacks = 8;  // U at most: pairs of 2048 bf16 or 1024 fp32 entries
 
 template <typename T, bool SHIFTED, bool REVERSE, int U>
-__global__ void __launch_bounds__(kShortNT) distill_short_kernel(DistillArgs a) {
+__global__ void __launch_bounds__(kShortNT, 4) distill_short_kernel(DistillArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t r = (int64_t)blockIdx.x * (kShortNT / 32) + (threadIdx.x >> 5);
   if (r >= a.B * a.K) return;
@@ -532,7 +534,7 @@ cudaError_t launch_long(const DistillArgs &a, int S, cudaStream_t stream) {
 }
 
 template <typename T, bool SHIFTED, bool REVERSE>
-cudaError_t plan(const DistillArgs &a, int S, cudaStream_t stream) {
+cudaError_t plan(const DistillArgs &a, int sms, int S, cudaStream_t stream) {
   constexpr int kVW = Elem<T>::kPerVec;
   // packs of a row, wherever it begins
   const int64_t packs = ((int64_t)a.V + (SHIFTED ? 2 : 1) * (kVW - 1)) / kVW;
@@ -547,17 +549,23 @@ cudaError_t plan(const DistillArgs &a, int S, cudaStream_t stream) {
           <<<(unsigned)ctas, kShortNT, 0, stream>>>(a);
     return cudaGetLastError();
   }
+  // CTAs per pair: so many that each takes 4096 packs of a row at most (32 KB chunks of
+  // the 48 KB held, the rest read again from L2), more while one wave of 4 CTAs per SM
+  // has room for them, 8 at most.
   if (S == 0) {
-    const int64_t need = (packs + kBuffers * kChunk - 1) / (kBuffers * kChunk);
-    S = need < 8 ? (int)need : 8;
+    const int64_t pairs = a.B * a.K;
+    S = (int)std::min<int64_t>((packs + 4095) / 4096, 8);
+    const int64_t room = std::min<int64_t>(4 * sms / pairs, packs / 512);
+    if (S < room) S = (int)std::min<int64_t>(room, 8);
   }
   while (S > 1 && a.B * a.K * S > INT32_MAX) S /= 2;
   return launch_long<T, SHIFTED, REVERSE>(a, S, stream);
 }
 
 template <typename T, bool SHIFTED>
-cudaError_t plan(const DistillArgs &a, int reverse, int S, cudaStream_t stream) {
-  return reverse ? plan<T, SHIFTED, true>(a, S, stream) : plan<T, SHIFTED, false>(a, S, stream);
+cudaError_t plan(const DistillArgs &a, int reverse, int sms, int S, cudaStream_t stream) {
+  return reverse ? plan<T, SHIFTED, true>(a, sms, S, stream)
+                 : plan<T, SHIFTED, false>(a, sms, S, stream);
 }
 
 template <typename T, bool SHIFTED, bool REVERSE>
@@ -586,7 +594,7 @@ cudaError_t distill_prepare() {
   return e == cudaSuccess ? prepare<uint16_t>() : e;
 }
 
-cudaError_t distill_launch(const DistillArgs &a, int dtype_bf16, int reverse, int S,
+cudaError_t distill_launch(const DistillArgs &a, int dtype_bf16, int reverse, int sms, int S,
                            cudaStream_t stream) {
   // Every row of all three arrays begins on a 16-byte boundary where their
   // addresses, the strides and V in bytes are multiples of 16.
@@ -596,10 +604,10 @@ cudaError_t distill_launch(const DistillArgs &a, int dtype_bf16, int reverse, in
       (uint64_t)(a.target_stride_b | a.target_stride_k | a.draft_stride_b | a.draft_stride_k | a.V) *
           (dtype_bf16 ? 2 : 4);
   if (dtype_bf16)
-    return bits % 16 == 0 ? plan<uint16_t, false>(a, reverse, S, stream)
-                          : plan<uint16_t, true>(a, reverse, S, stream);
-  return bits % 16 == 0 ? plan<float, false>(a, reverse, S, stream)
-                        : plan<float, true>(a, reverse, S, stream);
+    return bits % 16 == 0 ? plan<uint16_t, false>(a, reverse, sms, S, stream)
+                          : plan<uint16_t, true>(a, reverse, sms, S, stream);
+  return bits % 16 == 0 ? plan<float, false>(a, reverse, sms, S, stream)
+                        : plan<float, true>(a, reverse, sms, S, stream);
 }
 
 }  // namespace specv

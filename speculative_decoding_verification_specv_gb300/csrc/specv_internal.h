@@ -322,8 +322,8 @@ struct DistillArgs {
   void *out_grad;            // [B][K][V] contiguous, or null: the loss alone
 };
 cudaError_t distill_prepare();
-// S: CTAs per row pair, 0 = the library's choice
-cudaError_t distill_launch(const DistillArgs &a, int dtype_bf16, int reverse, int S,
+// S: CTAs per row pair, 0 = the library's choice for a device of `sms` SMs
+cudaError_t distill_launch(const DistillArgs &a, int dtype_bf16, int reverse, int sms, int S,
                            cudaStream_t stream);
 
 // Arguments of the clipping kernels: up to CAP gradients per launch, passed by value
