@@ -9,12 +9,27 @@
 //   T = sum e^{a} (a - c),  a = z - r of the leading row, c of the other one,
 // so that L / w = T / S_a - ln S_a + ln S_c; pass 2 writes the gradient.
 //
-// S CTAs (a cluster) share a pair of rows, each the same run of both.  A thread
-// keeps its entries of both rows in registers from the first pass to the second
-// (a tile of kRegs registers per row and thread), so a pair that fits the
-// cluster's registers is read once; of a longer one all but the last tile is read
-// again, from L2.  One cluster barrier lies between the passes: every warp sends
-// its partial sums to every CTA of the cluster, and each warp merges all of them.
+//
+// Long rows.  S CTAs (a cluster) share a pair, each the same run of both rows, cut
+// into chunks of 4 KB per row.  An issuing warp brings the chunks into shared memory
+// with bulk copies, six of them ahead of the 128 consuming threads; after pass 1 the
+// last six are still there for pass 2, the others are copied again (from L2: 1.02 to
+// 1.08 of the rows' bytes leave DRAM).  Between the passes every warp sends its partial
+// sums to every CTA of the cluster, and each warp merges all of them: one cluster
+// barrier.  Rows that lie off the 16-byte boundaries are joined from whole vectors as
+// they are read from shared memory.
+//
+// What bounds it.  2048 pairs of 128256 fp32 entries take 567 us (3.15 GB, 5.56 TB/s,
+// 0.82 of the copy peak), 1024 of bf16 164 us (0.79 GB, 4.80 TB/s).  The consuming warps
+// issue 0.45 (fp32) and 0.65 (bf16) of the time: four exponentials and some thirty
+// instructions per entry pair.  Of a CTA's time at 2048 fp32 pairs 13 % go by until its
+// first chunk is there, 38 % in pass 1, 18 % in the cluster barrier, 28 % in pass 2
+// (clock stamps), which the other CTAs of the SM cover only in part.  Tried and not
+// kept: the pair in registers instead (715 us with S = 8), register double buffers (841),
+// clusters that stay and copy ahead into their next pair (607), 16 KB chunks or more
+// threads with fewer CTAs per SM (570 to 750), sums without a maximum search (574).
+//
+// Short rows: a warp holds a pair in registers.
 #include <algorithm>
 
 #include <cooperative_groups.h>
@@ -73,14 +88,21 @@ __device__ __forceinline__ void merge_lanes(PairSums &y) {
   }
 }
 
+// log2 of a positive normal number: exactly the exponent, and the SFU's logarithm
+// (absolute error near 2^-22 there) of a mantissa in [0.75, 1.5).
+__device__ __forceinline__ float log2_of(float s) {
+  const int bits = __float_as_int(s), e = (bits - 0x3f400000) >> 23;
+  return lg2(__int_as_float(bits - (e << 23))) + (float)e;
+}
+
 // What follows from a pair's sums.
 template <bool REVERSE>
 __device__ __forceinline__ Merged merged(const PairSums &y) {
   Merged m;
   const bool bad = !(y.st < INFINITY) || !(y.sq < INFINITY);
   m.empty = !bad && (y.st == 0.0f || y.sq == 0.0f);
-  m.lt = lg2(y.st);
-  m.lq = lg2(y.sq);
+  m.lt = log2_of(y.st);
+  m.lq = log2_of(y.sq);
   m.rt = y.rt;
   m.rq = y.rq;
   const float mean = __fdividef(y.t, REVERSE ? y.sq : y.st);
@@ -208,6 +230,7 @@ __device__ __forceinline__ void gradient(const GradTerms &g, const TileT &xt, Ti
 constexpr int kShortNT = 128;
 constexpr int kShortPacks = 8;  // U at most: pairs of 2048 bf16 or 1024 fp32 entries
 
+// (four CTAs per SM: 12495 pairs of 1513 bf16 entries 40 us, with 165 registers 56)
 template <typename T, bool SHIFTED, bool REVERSE, int U>
 __global__ void __launch_bounds__(kShortNT, 4) distill_short_kernel(DistillArgs a) {
   const int lane = threadIdx.x & 31;
@@ -273,8 +296,8 @@ struct __align__(16) DistillShared {
   int lost;  // set when a copy did not land in time
 };
 
-// A thread's packs of a chunk, read from shared memory.  Edge packs are read from the
-// row; `inner`: the chunk has none, and no end.
+// A thread's packs of a chunk, read from shared memory.  `inner`: the chunk's packs are
+// whole in every row, and it has no end; else entries outside the row become -inf.
 template <typename T, bool SHIFTED>
 struct ChunkTile {
   static constexpr int kPairs = kUnroll * Elem<T>::kPerVec / 2;
@@ -341,7 +364,7 @@ __device__ __forceinline__ bool wait_suspended(uint64_t *bar, uint32_t parity) {
     if (it == 0) t0 = global_timer_ns();
     if (global_timer_ns() - t0 > kWaitLimitNs) break;
   }
-  return false;
+  return mbar_try_wait(bar, parity);  // (the time may have passed while the GPU was lent out)
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
@@ -398,7 +421,7 @@ __global__ void __launch_bounds__(kNT + 32, 4) distill_kernel(DistillArgs a, int
   // Chunk c goes to buffer c mod kBuffers.  The copies run 0 .. n-1 for pass 1, then
   // n-kBuffers-1 .. 0 for pass 2, which begins with the chunks still held.  The m-th
   // copy into a buffer completes phase m of its `full` barrier and waits for phase
-  // m-1 of its `empty` one.  `loads` of a chunk: m in pass 1, and in pass 2.
+  // m-1 of its `empty` one; load_1 and load_2 are the m of a chunk in each pass.
   auto load_1 = [&](int c) { return c / kBuffers; };
   auto load_2 = [&](int c) {
     const int held = (n - 1 - c % kBuffers) / kBuffers;  // copies before the held chunk's
@@ -549,9 +572,11 @@ cudaError_t plan(const DistillArgs &a, int sms, int S, cudaStream_t stream) {
           <<<(unsigned)ctas, kShortNT, 0, stream>>>(a);
     return cudaGetLastError();
   }
-  // CTAs per pair: so many that each takes 4096 packs of a row at most (32 KB chunks of
-  // the 48 KB held, the rest read again from L2), more while one wave of 4 CTAs per SM
-  // has room for them, 8 at most.
+  // CTAs per pair: so many that each takes 4096 packs of a row at most, more while one
+  // wave of 4 CTAs per SM has room for them, 8 at most.  More CTAs hold more of the pair
+  // but wait longer for one another.  Measured, us: 2048 pairs of 32064 packs S = 8 565,
+  // 6 614, 4 667; 1024 of 16032 S = 4 164, 8 177, 2 182; 396 of 9760 S = 3 48, 6 53, 1 55;
+  // 1776 of 3019 S = 1 55, 2 64; 34 of 14540 S = 8 11.6, 4 16, 2 28.
   if (S == 0) {
     const int64_t pairs = a.B * a.K;
     S = (int)std::min<int64_t>((packs + 4095) / 4096, 8);

@@ -156,6 +156,25 @@ def test_logprobs_special_rows_in_clusters(specv, cluster_env, S):
             _check_logprobs(specv, z, x, top)
 
 
+@pytest.mark.parametrize("dtype,period,width", [("bf16", 2048, 8), ("f32", 1024, 4)])
+def test_logprobs_crowded_rows(specv, cluster_env, dtype, period, width):
+    """Rows whose largest entries all fall to one thread of the streaming loop: more of
+    them than the selection collects, so that the repeated search decides."""
+    os.environ["SPECV_CLUSTER_SIZE"] = "1"
+    V = 160001
+    r = torch.arange(V, device=DEV, dtype=torch.float32)
+    z = _randn((V,), 7)
+    big = r % period < width
+    rows = [torch.where(big, 40.0 + (r * 13 % 61) * 0.25, z),   # with many ties
+            torch.where(big, 40.0 + r * 1e-4, z),               # rising
+            torch.where(big, 90.0 - r * 1e-4, z),               # falling
+            torch.where(big, z.abs() + 30.0, z).masked_fill(r % 3 == 1, NEG)]
+    z = torch.stack(rows).to(DT[dtype])
+    x = torch.full((len(rows),), 5, dtype=torch.int32, device=DEV)
+    for top in (1, 20, 32):
+        _check_logprobs(specv, z, x, top)
+
+
 def test_logprobs_invalid_and_absent_tokens(specv):
     for V in (40, 3001, 50000):
         z = _randn((2, 5, V), 3)
