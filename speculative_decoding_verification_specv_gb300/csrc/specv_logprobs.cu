@@ -11,13 +11,14 @@
 // row, each an equal run of its 16-byte vectors; thread t of a CTA takes every
 // NT-th vector of the run: its strip.  The streaming loop keeps S and T about a
 // reference that follows the strip's maximum only when that has risen by more
-// than kLazy, and, of the alternatives, nothing but the strip's maximum and the
-// vector that first held it (two instructions per vector).  After the loop
+// than kLazy, and, of the alternatives, nothing but the maximum and the vector that
+// first held it (two instructions per vector), for the whole strip or for each of its
+// eight segments (long rows, several alternatives).  After the loop
 //   1. the 32 largest strip maxima over groups of NT / 32 threads are sorted, and
 //      the top_n-th, as the pair (value, vector), is the threshold: at least
 //      top_n entries are no worse, one in each of as many strips;
-//   2. the strips that reach it, about top_n of NT, are read again (L2 still has
-//      them) and their entries that reach it are collected;
+//   2. the strips or segments that reach it, about top_n of them, are read again and
+//      their entries that reach it are collected;
 //   3. a warp sorts those and keeps the first top_n.
 // An entry worse than the threshold has top_n better ones, so none is missed; the
 // pair's order makes equal values, a constant row for instance, select top_n
@@ -39,17 +40,20 @@ namespace {
 
 constexpr int kUnroll = 4;      // vectors in flight per thread, and as many being folded
 constexpr int kCand = 512;      // entries collected above the threshold
+constexpr int kSegTop = 5;          // strips are cut into segments from so many alternatives on ...
+constexpr int kSegVectors = 12288;  // ... in rows of so many vectors
 // Terms may exceed the reference by e^8: sums stay far from overflow (2^31 e^8 <
 // 10^13), and a strip of ordinary logits moves its reference once or twice.
 constexpr float kLazy = 8.0f;
 
-template <int NT, bool CLUSTER>
+template <int NT, bool CLUSTER, int SEGS>
 struct LogprobShared {
   float red[NT / 32][3];
   uint64_t group[32];
   uint64_t tau;
   int n_strips, n_cand;
-  int strips[NT];
+  uint64_t keys[SEGS > 1 ? SEGS : 1][SEGS > 1 ? NT : 1];  // of every segment
+  uint16_t strips[NT * SEGS];                              // thread + NT * segment
   uint64_t cand[kCand];
   uint64_t best[NT / 32];
   float4 part[CLUSTER ? kMaxCluster : 1];
@@ -60,7 +64,7 @@ struct LogprobShared {
 struct StripSums {
   float ref = -3.402823466e38f;  // the reference of s and t (finite, or +inf)
   uint64_t s = 0, t = 0;         // packed partial sums
-  float top = -INFINITY;         // the strip's maximum ...
+  float top = -INFINITY;         // the segment's maximum ...
   int top_vec = 0;               // ... and the first vector that holds it
 };
 
@@ -98,10 +102,10 @@ __device__ __forceinline__ void fold(StripSums &a, const uint4 (&v)[U], int k, i
 
 // The CTA's top_n largest keys among the strips of vectors [lo, hi): lane i of warp
 // 0 returns the i-th.  Every thread calls it.
-template <typename T, int NT, bool CLUSTER>
-__device__ __forceinline__ uint64_t select_top(LogprobShared<NT, CLUSTER> &sh,
+template <typename T, int NT, bool CLUSTER, int SEGS>
+__device__ __forceinline__ uint64_t select_top(LogprobShared<NT, CLUSTER, SEGS> &sh,
                                                const RowVectors<T> &row, int lo, int hi, int top_n,
-                                               uint64_t strip_key) {
+                                               int segs, int seg_vecs, uint64_t strip_key) {
   constexpr int kGroup = NT / 32;
   constexpr int VW = Elem<T>::kPerVec;
   const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -117,14 +121,20 @@ __device__ __forceinline__ uint64_t select_top(LogprobShared<NT, CLUSTER> &sh,
   }
   __syncthreads();
   const uint64_t tau = sh.tau;  // 0: fewer than top_n groups hold an entry, all entries count
-  if (strip_key != 0 && strip_key >= tau) sh.strips[atomicAdd(&sh.n_strips, 1)] = tid;
+  if (strip_key != 0 && strip_key >= tau)
+    for (int g = 0; g < segs; ++g) {
+      const uint64_t k = SEGS > 1 ? sh.keys[g][tid] : strip_key;
+      if (k != 0 && k >= tau) sh.strips[atomicAdd(&sh.n_strips, 1)] = (uint16_t)(tid + NT * g);
+    }
   __syncthreads();
   const float t_value = tau == 0 ? -INFINITY : key_value(tau);
   const int t_vec = tau == 0 ? -1 : (int)key_index(tau);
-  const int n_strips = sh.n_strips, per_strip = (hi - lo + NT - 1) / NT;
-  for (int64_t i = tid; i < (int64_t)n_strips * per_strip; i += NT) {
-    const int s = (int)(i / per_strip);
-    const int k = lo + sh.strips[s] + (int)(i - (int64_t)s * per_strip) * NT;
+  const int n_strips = sh.n_strips;
+  for (int64_t i = tid; i < (int64_t)n_strips * seg_vecs; i += NT) {
+    const int s = (int)(i / seg_vecs), at = sh.strips[s];
+    const int64_t of = (int64_t)(at / NT) * seg_vecs + (i - (int64_t)s * seg_vecs);
+    const int64_t k64 = lo + at % NT + of * NT;
+    const int k = k64 < hi ? (int)k64 : hi;
     if (k >= hi) continue;
     const uint4 v = row.load(k);
 #pragma unroll
@@ -172,10 +182,10 @@ __device__ __forceinline__ uint64_t select_top(LogprobShared<NT, CLUSTER> &sh,
   return top;
 }
 
-template <typename T, int NT, bool CLUSTER>
+template <typename T, int NT, bool CLUSTER, int SEGS>
 __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 1024 / NT)
     logprobs_kernel(LogprobArgs a, int S) {
-  __shared__ LogprobShared<NT, CLUSTER> sh;
+  __shared__ LogprobShared<NT, CLUSTER, SEGS> sh;
   const int64_t r = CLUSTER ? (int64_t)blockIdx.x / S : (int64_t)blockIdx.x;
   const int rank = CLUSTER ? (int)cg::this_cluster().block_rank() : 0;
   const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -221,20 +231,37 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 1024 / NT)
       }
     }
   };
+  const int batches = (hi - lo + kBatch - 1) / kBatch;
+  const int seg_batches = max(1, (batches + SEGS - 1) / SEGS);
+  int segs = 0;
+  uint64_t strip_key = 0;  // the strip's maximum (0: it has none)
   uint4 cur[kUnroll], next[kUnroll];
   load_batch(lo, cur);
-  for (int base = lo; base < hi; base += kBatch) {
-    const bool more = hi - base > kBatch;
-    if (more) load_batch(base + kBatch, next);
-    fold<T, kUnroll>(sums, cur, base + tid, NT);
-    if (more) {
+  for (int base = lo; base < hi;) {
+    const int stop = SEGS > 1 && hi - base > seg_batches * kBatch ? base + seg_batches * kBatch : hi;
+    for (; base < stop; base += kBatch) {
+      const bool more = hi - base > kBatch;
+      if (more) load_batch(base + kBatch, next);
+      fold<T, kUnroll>(sums, cur, base + tid, NT);
+      if (more) {
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) cur[u] = next[u];
+        for (int u = 0; u < kUnroll; ++u) cur[u] = next[u];
+      }
     }
+    const uint64_t key = sums.top > -INFINITY ? order_key(sums.top, (uint32_t)sums.top_vec) : 0;
+    if (SEGS > 1) {
+      sh.keys[segs][tid] = key;
+      sums.top = -INFINITY;
+    } else {
+      strip_key = key;
+    }
+    ++segs;
   }
+  if (SEGS > 1)
+    for (int g = 0; g < segs; ++g) strip_key = max_u64(strip_key, sh.keys[g][tid]);
 
   // ------------------------------------------------------------------ merge: the CTA
-  float M = sums.top, s, t, s1, t1;
+  float M = strip_key != 0 ? key_value(strip_key) : -INFINITY, s, t, s1, t1;
   unpack2(sums.s, s, s1);
   unpack2(sums.t, t, t1);
   s += s1;
@@ -254,8 +281,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 1024 / NT)
   }
   uint64_t top = 0;  // lane i of warp 0: the i-th largest key
   if (top_n > 0)
-    top = select_top<T>(sh, row, lo, hi, top_n,
-                        sums.top > -INFINITY ? order_key(sums.top, (uint32_t)sums.top_vec) : 0);
+    top = select_top<T>(sh, row, lo, hi, top_n, segs, seg_batches * kUnroll, strip_key);
   else
     __syncthreads();
   if (warp == 0) {
@@ -398,7 +424,7 @@ __global__ void __launch_bounds__(kGradNT) logprobs_grad_kernel(LogprobGradArgs 
   }
 }
 
-template <typename T, int NT, bool CLUSTER>
+template <typename T, int NT, bool CLUSTER, int SEGS>
 cudaError_t launch_forward(const LogprobArgs &a, int S, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.R * S), 1, 1);
@@ -411,7 +437,7 @@ cudaError_t launch_forward(const LogprobArgs &a, int S, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CLUSTER ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, NT, CLUSTER>, a, S);
+  return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, NT, CLUSTER, SEGS>, a, S);
 }
 
 template <typename T>
@@ -419,7 +445,7 @@ cudaError_t forward(const LogprobArgs &a, int sms, int S, cudaStream_t stream) {
   constexpr int kVW = Elem<T>::kPerVec;
   const int64_t vectors = (a.V + kVW - 1) / kVW;
   // Short rows: a warp per row, up to 8 vectors per lane.
-  if (S == 0 && vectors <= 32 * 8) return launch_forward<T, 32, false>(a, 1, stream);
+  if (S == 0 && vectors <= 32 * 8) return launch_forward<T, 32, false, 1>(a, 1, stream);
   // CTAs per row: as many as one wave of 4 CTAs per SM allows, up to 8, each with 1200
   // vectors at least (a batch of the streaming loop is 1024).  Measured: 9 rows of
   // 16032 vectors 6.6 us with S = 8, 7.8 with 16, 12.3 with 1; 185 rows of 12501 15.9
@@ -430,17 +456,23 @@ cudaError_t forward(const LogprobArgs &a, int sms, int S, cudaStream_t stream) {
     S = (int)std::max<int64_t>(1, std::min<int64_t>(most, 8));
   }
   while (S > 1 && a.R * S > INT32_MAX) S /= 2;
-  return S == 1 ? launch_forward<T, 256, false>(a, 1, stream)
-                : launch_forward<T, 256, true>(a, S, stream);
+  if (S > 1) return launch_forward<T, 256, true, 1>(a, S, stream);
+  // Segments, for several alternatives of long rows: what is read again of a strip,
+  // from DRAM in a batch whose rows overfill L2, is then an eighth.  2304 rows of
+  // 128256 entries, us with and without: fp32 20 alternatives 199 and 279, 5 189 and
+  // 198, 1 187 and 184; bf16 20 126 and 145, 5 117 and 116, 1 115 and 110.
+  return a.top_n >= kSegTop && vectors >= kSegVectors
+             ? launch_forward<T, 256, false, 8>(a, 1, stream)
+             : launch_forward<T, 256, false, 1>(a, 1, stream);
 }
 
 }  // namespace
 
 cudaError_t logprobs_prepare() {
-  cudaError_t e = cudaFuncSetAttribute(logprobs_kernel<float, 256, true>,
+  cudaError_t e = cudaFuncSetAttribute(logprobs_kernel<float, 256, true, 1>,
                                        cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(logprobs_kernel<uint16_t, 256, true>,
+    e = cudaFuncSetAttribute(logprobs_kernel<uint16_t, 256, true, 1>,
                              cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   return e;
 }
