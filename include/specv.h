@@ -533,8 +533,10 @@ typedef enum {
  * of positive q.  A
  * pair in which either row masks every entry has no divergence: loss 0, gradient
  * 0.  A NaN or +inf logit gives NaN for its pair.  Sums are fp32; a loss below
- * zero by rounding is written as 0.  No scratch, no allocation; asynchronous on
- * `stream`; host argument errors return SPECV_ERR_INVALID_ARG, launching nothing.
+ * zero by rounding is written as 0.  (A copy into shared memory that does not land
+ * within 200 ms, which is not expected, makes its pair NaN.)  No scratch, no
+ * allocation; asynchronous on `stream`; host argument errors return
+ * SPECV_ERR_INVALID_ARG, launching nothing.
  */
 specv_status specv_distill(const void *target_logits, const void *draft_logits,
                            const float *weight, int64_t B, int32_t K, int32_t V,
