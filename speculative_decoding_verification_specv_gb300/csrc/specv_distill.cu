@@ -9,22 +9,21 @@
 //   T = sum e^{a} (a - c),  a = z - r of the leading row, c of the other one,
 // so that L / w = T / S_a - ln S_a + ln S_c; pass 2 writes the gradient.
 //
-//
 // Long rows.  S CTAs (a cluster) share a pair, each the same run of both rows, cut
 // into chunks of 4 KB per row.  An issuing warp brings the chunks into shared memory
-// with bulk copies, six of them ahead of the 128 consuming threads; after pass 1 the
-// last six are still there for pass 2, the others are copied again, most of them from
-// L2.  Between the passes every warp sends its partial sums to every CTA of the
-// cluster, and each warp merges all of them: one cluster
-// barrier.  Rows that lie off the 16-byte boundaries are joined from whole vectors as
-// they are read from shared memory.
+// with bulk copies, six or four of them ahead of the 128 consuming threads; after pass
+// 1 these last ones are still there for pass 2, the others are copied again, nearly all
+// from L2 (1.02 of the rows' bytes leave DRAM).  Between the passes every warp sends
+// its partial sums to every CTA of the cluster, and each warp merges all of them: one
+// cluster barrier.  Rows that lie off the 16-byte boundaries are joined from whole
+// vectors as they are read from shared memory.
 //
-// What bounds it.  2048 pairs of 128256 fp32 entries take 567 us (3.15 GB, 5.56 TB/s,
-// 0.82 of the copy peak), 1024 of bf16 164 us (0.79 GB, 4.80 TB/s).  The consuming warps
-// issue 0.45 (fp32) and 0.65 (bf16) of the time: four exponentials and some thirty
-// instructions per entry pair.  Of a CTA's time at 2048 fp32 pairs 13 % go by until its
-// first chunk is there, 38 % in pass 1, 18 % in the cluster barrier, 28 % in pass 2
-// (clock stamps), which the other CTAs of the SM cover only in part.  Tried and not
+// What bounds it.  2048 pairs of 128256 fp32 entries take 541 us (3.15 GB, 5.8 TB/s,
+// 0.86 of the copy peak), 1024 of bf16 155 us (0.79 GB, 5.1 TB/s).  The warps issue 0.46
+// (fp32) and 0.67 (bf16) of the time, at four exponentials and some thirty instructions
+// per entry pair.  Of a CTA's time at 2048 fp32 pairs 13 % go by until its first chunk
+// is there, 38 % in pass 1, 18 % in the cluster barrier, 28 % in pass 2 (clock stamps,
+// four CTAs per SM), which the other CTAs of the SM cover only in part.  Tried and not
 // kept: the pair in registers instead (715 us with S = 8), register double buffers (841),
 // clusters that stay and copy ahead into their next pair (607), 16 KB chunks or more
 // threads with fewer CTAs per SM (570 to 750), sums without a maximum search (574).
@@ -287,12 +286,13 @@ constexpr int kNT = 128;     // consuming threads; one more warp issues the copi
 constexpr int kUnroll = 2;   // packs per thread of a chunk
 constexpr int kChunk = kNT * kUnroll;              // packs of a chunk
 constexpr int kChunkBytes = (kChunk + 1) * 16;     // a shifted row's chunk needs one vector more
-constexpr int kBuffers = 6;                        // chunks of both rows held per CTA
 
+// BUFFERS: chunks of both rows held per CTA, MIN_CTAS: CTAs per SM that leaves room for.
+template <int BUFFERS>
 struct __align__(16) DistillShared {
   float4 a[kMaxCluster * (kNT / 32)];  // (rt, st, rq, sq) of every warp of the cluster
   float t[kMaxCluster * (kNT / 32)];
-  uint64_t full[kBuffers], empty[kBuffers];
+  uint64_t full[BUFFERS], empty[BUFFERS];
   int lost;  // set when a copy did not land in time
 };
 
@@ -381,11 +381,11 @@ __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-template <typename T, bool SHIFTED, bool REVERSE>
-__global__ void __launch_bounds__(kNT + 32, 4) distill_kernel(DistillArgs a, int S) {
-  constexpr int kNW = kNT / 32;
+template <typename T, bool SHIFTED, bool REVERSE, int BUFFERS, int MIN_CTAS>
+__global__ void __launch_bounds__(kNT + 32, MIN_CTAS) distill_kernel(DistillArgs a, int S) {
+  constexpr int kNW = kNT / 32, kBuffers = BUFFERS;
   extern __shared__ __align__(16) unsigned char chunks[];  // [kBuffers][2][kChunkBytes]
-  __shared__ DistillShared sh;
+  __shared__ DistillShared<BUFFERS> sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = S > 1 ? (int)cluster.block_rank() : 0;
   const int64_t r = (int64_t)blockIdx.x / S;
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kNT + 32, 4) distill_kernel(DistillArgs a, int
   if (warp == kNW) {  // ------------------------------------------- the issuing warp
     bool fine = true;
     // what is read again is kept in L2 rather than what is not (2048 pairs of 128256
-    // fp32 entries: 549 us, without 567)
+    // fp32 entries, six chunks held: 549 us, without 567)
     uint64_t keep, drop;
     asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
     asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(drop));
@@ -555,12 +555,12 @@ __global__ void __launch_bounds__(kNT + 32, 4) distill_kernel(DistillArgs a, int
   }
 }
 
-template <typename T, bool SHIFTED, bool REVERSE>
+template <typename T, bool SHIFTED, bool REVERSE, int BUFFERS, int MIN_CTAS>
 cudaError_t launch_long(const DistillArgs &a, int S, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.B * a.K * S), 1, 1);
   cfg.blockDim = dim3(kNT + 32, 1, 1);
-  cfg.dynamicSmemBytes = kBuffers * 2 * kChunkBytes;
+  cfg.dynamicSmemBytes = BUFFERS * 2 * kChunkBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -569,7 +569,7 @@ cudaError_t launch_long(const DistillArgs &a, int S, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = S > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, distill_kernel<T, SHIFTED, REVERSE>, a, S);
+  return cudaLaunchKernelEx(&cfg, distill_kernel<T, SHIFTED, REVERSE, BUFFERS, MIN_CTAS>, a, S);
 }
 
 template <typename T, bool SHIFTED, bool REVERSE>
@@ -600,7 +600,13 @@ cudaError_t plan(const DistillArgs &a, int sms, int S, cudaStream_t stream) {
     if (S < room) S = (int)std::min<int64_t>(room, 8);
   }
   while (S > 1 && a.B * a.K * S > INT32_MAX) S /= 2;
-  return launch_long<T, SHIFTED, REVERSE>(a, S, stream);
+  // Six chunks held and four CTAs per SM where that is one wave, else four and six: a
+  // full GPU gains more from CTAs than from what they hold.  Us, six held and four: 1024
+  // pairs of 16032 packs 161 and 155, 2048 of 32064 560 and 550, 880 of 3429 (joined)
+  // 48.5 and 43.4, 9207 of 1140 127 and 116; 133 of 6251 (joined) 16.3 and 17.5, 24 of
+  // 12545 8.7 and 9.7.
+  if (a.B * a.K * S <= 4 * sms) return launch_long<T, SHIFTED, REVERSE, 6, 4>(a, S, stream);
+  return launch_long<T, SHIFTED, REVERSE, 4, 6>(a, S, stream);
 }
 
 template <typename T, bool SHIFTED>
@@ -609,22 +615,27 @@ cudaError_t plan(const DistillArgs &a, int reverse, int sms, int S, cudaStream_t
                  : plan<T, SHIFTED, false>(a, sms, S, stream);
 }
 
-template <typename T, bool SHIFTED, bool REVERSE>
+template <typename T, bool SHIFTED, bool REVERSE, int BUFFERS, int MIN_CTAS>
 cudaError_t prepare_one() {
-  cudaError_t e = cudaFuncSetAttribute(distill_kernel<T, SHIFTED, REVERSE>,
-                                       cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  const auto kernel = distill_kernel<T, SHIFTED, REVERSE, BUFFERS, MIN_CTAS>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(distill_kernel<T, SHIFTED, REVERSE>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kBuffers * 2 * kChunkBytes);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             BUFFERS * 2 * kChunkBytes);
   return e;
+}
+template <typename T, bool SHIFTED, bool REVERSE>
+cudaError_t prepare_both() {
+  const cudaError_t e = prepare_one<T, SHIFTED, REVERSE, 6, 4>();
+  return e == cudaSuccess ? prepare_one<T, SHIFTED, REVERSE, 4, 6>() : e;
 }
 template <typename T>
 cudaError_t prepare() {
-  cudaError_t e = prepare_one<T, false, false>();
-  if (e == cudaSuccess) e = prepare_one<T, false, true>();
-  if (e == cudaSuccess) e = prepare_one<T, true, false>();
-  if (e == cudaSuccess) e = prepare_one<T, true, true>();
+  cudaError_t e = prepare_both<T, false, false>();
+  if (e == cudaSuccess) e = prepare_both<T, false, true>();
+  if (e == cudaSuccess) e = prepare_both<T, true, false>();
+  if (e == cudaSuccess) e = prepare_both<T, true, true>();
   return e;
 }
 

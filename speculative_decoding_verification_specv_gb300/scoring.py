@@ -36,6 +36,7 @@ class TokenLogprobs(NamedTuple):
 # points are looked up once, a tensor that fits is passed with a single test, and the
 # stream's handle is asked for without building a Stream object.
 _CODES = {torch.float32: F32, torch.bfloat16: BF16}
+_Tensor, _empty, _f32, _i32 = torch.Tensor, torch.empty, torch.float32, torch.int32
 _entries: dict = {}
 
 
@@ -54,14 +55,14 @@ def _stream(stream, dev) -> int:
 
 def _fit(t, name: str, dtype, shape, dev):
     """A contiguous tensor of this type, shape and device, else the error that says why."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape
             and t.device == dev and t.is_contiguous()):
         _require(t, name, dtype, shape, dev)
 
 
 def _rows(t: torch.Tensor, name: str):
     """(B, N, V, stride_b, stride_n) of logits [B][N][V] or [N][V] on the GPU."""
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() == 3:
         (B, N, V), (sb, sn, sv) = t.shape, t.stride()
@@ -92,17 +93,17 @@ def token_logprobs(logits, tokens, top_n: int = 0, stream=None) -> TokenLogprobs
     B, N, V, sb, sn = _rows(logits, "logits")
     dev, lead = logits.device, logits.shape[:-1]
     code = _dtype_code(logits)
-    _fit(tokens, "tokens", torch.int32, lead, dev)
+    _fit(tokens, "tokens", _i32, lead, dev)
     n = int(top_n)
     if not 0 <= n <= MAX_TOP:
         raise ValueError(f"top_n must be in 0..{MAX_TOP}")
-    logprobs = torch.empty(lead, dtype=torch.float32, device=dev)
-    entropy = torch.empty(lead, dtype=torch.float32, device=dev)
-    stats = torch.empty((*lead, 2), dtype=torch.float32, device=dev)
+    logprobs = _empty(lead, dtype=_f32, device=dev)
+    entropy = _empty(lead, dtype=_f32, device=dev)
+    stats = _empty((*lead, 2), dtype=_f32, device=dev)
     top_t = top_l = None
     if n:
-        top_t = torch.empty((*lead, n), dtype=torch.int32, device=dev)
-        top_l = torch.empty((*lead, n), dtype=torch.float32, device=dev)
+        top_t = _empty((*lead, n), dtype=_i32, device=dev)
+        top_l = _empty((*lead, n), dtype=_f32, device=dev)
     st = _entry("specv_token_logprobs")(
         logits.data_ptr(), tokens.data_ptr(), B, N, V, sb, sn, code, n, logprobs.data_ptr(),
         entropy.data_ptr(), stats.data_ptr(), top_t.data_ptr() if n else None,
@@ -125,14 +126,14 @@ def token_logprobs_backward(logits, tokens, stats, entropy, grad_logprobs, grad_
     B, N, V, sb, sn = _rows(logits, "logits")
     dev, lead = logits.device, logits.shape[:-1]
     code = _dtype_code(logits)
-    _fit(tokens, "tokens", torch.int32, lead, dev)
-    _fit(stats, "stats", torch.float32, (*lead, 2), dev)
-    _fit(entropy, "entropy", torch.float32, lead, dev)
-    _fit(grad_logprobs, "grad_logprobs", torch.float32, lead, dev)
+    _fit(tokens, "tokens", _i32, lead, dev)
+    _fit(stats, "stats", _f32, (*lead, 2), dev)
+    _fit(entropy, "entropy", _f32, lead, dev)
+    _fit(grad_logprobs, "grad_logprobs", _f32, lead, dev)
     if grad_entropy is not None:
-        _fit(grad_entropy, "grad_entropy", torch.float32, lead, dev)
+        _fit(grad_entropy, "grad_entropy", _f32, lead, dev)
     if out is None:
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+        out = _empty(logits.shape, dtype=logits.dtype, device=dev)
     else:
         _fit(out, "out", logits.dtype, logits.shape, dev)
     st = _entry("specv_token_logprobs_backward")(
@@ -173,11 +174,11 @@ def distill(target_logits, draft_logits, weight=None, kind: int = FORWARD_KL, ne
         _fit(weight, "weight", torch.float32, (B, K), dev)
     if kind not in (FORWARD_KL, REVERSE_KL):
         raise ValueError("kind must be FORWARD_KL (0) or REVERSE_KL (1)")
-    loss = torch.empty((B, K), dtype=torch.float32, device=dev)
+    loss = _empty((B, K), dtype=_f32, device=dev)
     if out_grad is not None:
         _fit(out_grad, "out_grad", draft_logits.dtype, (B, K, V), dev)
     elif need_grad:
-        out_grad = torch.empty((B, K, V), dtype=draft_logits.dtype, device=dev)
+        out_grad = _empty((B, K, V), dtype=draft_logits.dtype, device=dev)
     st = _entry("specv_distill")(
         target_logits.data_ptr(), draft_logits.data_ptr(),
         None if weight is None else weight.data_ptr(), B, K, V, tsb, tsk, dsb, dsk, code,
@@ -219,7 +220,7 @@ def clip_grads(grads, max_norm: float, out=None, stream=None) -> torch.Tensor:
     table = array("q", bytes(32 * len(grads)))
     table[0::4], table[1::4] = array("q", at), array("q", to)
     table[2::4], table[3::4] = array("q", counts), array("q", codes)
-    norm = torch.empty((), dtype=torch.float32, device=dev)
+    norm = _empty((), dtype=_f32, device=dev)
     st = _entry("specv_clip_grads")(table.buffer_info()[0] if grads else None, len(grads), max_norm,
                                     norm.data_ptr(), _stream(stream, dev))
     if st:
