@@ -460,7 +460,8 @@ specv_status specv_verify_noalloc(const void *target_logits, const void *draft_l
  *   out_logprob    [B][N]  fp32   ln p(token)
  *   out_entropy    [B][N]  fp32   -sum_v p_v ln p_v
  *   out_stats      [B][N][2] fp32 (max_v z_v, ln sum_v exp(z_v - max)): their sum is the
- *                                 row's log-normaliser; kept for the gradient
+ *                                 row's log-normaliser; kept for the gradient;
+ *                                 8-byte aligned
  *   out_top_tokens [B][N][top_n] int32, out_top_logprobs [B][N][top_n] fp32:
  *                  the most likely entries in order, ties by the lower token
  *                  (both NULL when top_n == 0)
@@ -487,7 +488,8 @@ specv_status specv_token_logprobs(const void *logits, const int32_t *tokens, int
  *   out_grad[b][n][v] = g (1[v = token] - p_v) - h p_v (ln p_v + entropy).
  *
  *   logits, tokens, B, N, V, stride_b, stride_n, dtype   as the forward call
- *   stats [B][N][2], entropy [B][N]   what the forward call wrote
+ *   stats [B][N][2], entropy [B][N]   what the forward call wrote (stats 8-byte
+ *                                     aligned)
  *   grad_logprob [B][N]   fp32
  *   grad_entropy [B][N]   fp32, or NULL (zeros)
  *   out_grad     [B][N][V]  dtype, contiguous; may be `logits` itself when that
@@ -559,7 +561,7 @@ typedef struct {
  *   norm = sqrt(sum x^2),  c = min(1, max_norm / (norm + 1e-6)),  out = c x
  * (rounded once to the gradient's type).
  *
- *   grads     [n] on the HOST, read before the call returns; n >= 0
+ *   grads     [n] on the HOST, read before the call returns; 0 <= n <= 8 million
  *   max_norm  >= 0; +inf only measures
  *   out_norm  fp32, device: the norm before clipping
  *

@@ -2,7 +2,6 @@
 // in include/specv.h): log probabilities, distillation, gradient clipping.
 //
 // Host-side work only: argument validation, launch shapes, the launches.
-#include <cmath>
 #include <cstdint>
 
 #include <nvtx3/nvToolsExt.h>
@@ -46,6 +45,11 @@ bool dtype_ok(int64_t dtype) { return dtype == SPECV_F32 || dtype == SPECV_BF16;
 
 bool misaligned(const void *p, int64_t dtype) {
   return (uintptr_t)p % (dtype == SPECV_BF16 ? 2 : 4) != 0;
+}
+// 32-bit arrays (null ones pass)
+template <typename... P>
+bool words_misaligned(const P *...p) {
+  return (... || ((uintptr_t)p % 4 != 0));
 }
 
 // The launches of specv_clip_grads: the norm's, then the scaling's, each for up to CAP
@@ -107,6 +111,9 @@ specv_status specv_token_logprobs(const void *logits, const int32_t *tokens, int
     return SPECV_ERR_INVALID_ARG;
   if (top_n < 0 || top_n > specv::kMaxTop) return SPECV_ERR_INVALID_ARG;
   if (top_n > 0 && (!out_top_tokens || !out_top_logprobs)) return SPECV_ERR_INVALID_ARG;
+  if (words_misaligned(tokens, out_logprob, out_entropy, out_top_tokens, out_top_logprobs) ||
+      (uintptr_t)out_stats % sizeof(float2) != 0)  // written as pairs
+    return SPECV_ERR_INVALID_ARG;
   int sms = 0;
   const int ready = specv::device_ready(&sms);
   if (ready != SPECV_OK) return (specv_status)ready;
@@ -141,6 +148,9 @@ specv_status specv_token_logprobs_backward(const void *logits, const int32_t *to
   if (!view_ok(B, N, V, stride_b, stride_n) || !dtype_ok(dtype) || misaligned(logits, dtype) ||
       misaligned(out_grad, dtype))
     return SPECV_ERR_INVALID_ARG;
+  if (words_misaligned(tokens, entropy, grad_logprob, grad_entropy) ||
+      (uintptr_t)stats % sizeof(float2) != 0)  // read as pairs
+    return SPECV_ERR_INVALID_ARG;
   int sms = 0;
   const int ready = specv::device_ready(&sms);
   if (ready != SPECV_OK) return (specv_status)ready;
@@ -174,7 +184,7 @@ specv_status specv_distill(const void *target_logits, const void *draft_logits,
     return SPECV_ERR_INVALID_ARG;
   if (kind != SPECV_FORWARD_KL && kind != SPECV_REVERSE_KL) return SPECV_ERR_INVALID_ARG;
   if (misaligned(target_logits, dtype) || misaligned(draft_logits, dtype) ||
-      misaligned(out_grad, dtype))
+      misaligned(out_grad, dtype) || words_misaligned(weight, out_loss))
     return SPECV_ERR_INVALID_ARG;
   int sms = 0;
   const int ready = specv::device_ready(&sms);
@@ -202,6 +212,7 @@ specv_status specv_clip_grads(const specv_grad *grads, int64_t n, float max_norm
                               void *stream) {
   NvtxRange range("specv_clip_grads");
   if (n < 0 || (n > 0 && !grads) || !out_norm || !(max_norm >= 0.0f)) return SPECV_ERR_INVALID_ARG;
+  if (words_misaligned(out_norm)) return SPECV_ERR_INVALID_ARG;
   int64_t live = 0, elements = 0;  // gradients with elements, and those
   for (int64_t i = 0; i < n; ++i) {
     const specv_grad &g = grads[i];

@@ -28,7 +28,6 @@
 
 #include <cooperative_groups.h>
 
-#include "specv_block.cuh"
 #include "specv_internal.h"
 #include "specv_rowstat.cuh"
 

@@ -88,7 +88,7 @@ def token_logprobs(logits, tokens, top_n: int = 0, stream=None) -> TokenLogprobs
     lower token; masked (-inf) entries are none.  Rows with a NaN or +inf, or with
     a token outside [0, V), give NaN; rows that mask every entry a log probability
     of -inf and an entropy of 0.  Asynchronous on ``stream`` (default: the current
-    stream).
+    stream).  No autograd graph is recorded: token_logprobs_backward is the gradient.
     """
     B, N, V, sb, sn = _rows(logits, "logits")
     dev, lead = logits.device, logits.shape[:-1]

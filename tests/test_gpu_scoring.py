@@ -637,5 +637,8 @@ def test_scoring_refuses_bad_tensors(specv):
         specv.distill(z.bfloat16(), z)
     with pytest.raises(TypeError):
         specv.clip_grads([z.half()], 1.0)
+    odd = torch.zeros(13, device=DEV)[1:].view(2, 3, 2)  # contiguous, 4 bytes off a pair
+    with pytest.raises(specv.SpecvError):
+        specv.token_logprobs_backward(z, x, odd, f, f)
     with pytest.raises(specv.SpecvError):  # no rows
         specv.token_logprobs(z[:0], x[:0])

@@ -33,6 +33,26 @@ def test_token_logprobs_validates(kw):
     assert _logprobs(**kw) == 1
 
 
+def test_token_logprobs_checks_alignment():
+    for i in range(7):  # every array at 2 bytes off, the statistics also at 4
+        for off in (2, 4) if i == 4 else (2,):
+            p = [FAKE] * 7
+            p[i] += off
+            assert specv.raw_call("specv_token_logprobs", p[0], p[1], 2, 3, 100, 300, 100, 0, 2,
+                                  p[2], p[3], p[4], p[5], p[6], None) == 1, (i, off)
+    for i in range(7):
+        for off in (2, 4) if i == 2 else (2,):
+            p = [FAKE] * 7
+            p[i] += off
+            assert specv.raw_call("specv_token_logprobs_backward", *p[:6], 2, 3, 100, 300, 100, 0,
+                                  p[6], None) == 1, (i, off)
+    for i in range(5):
+        p = [FAKE] * 5
+        p[i] += 2
+        assert specv.raw_call("specv_distill", p[0], p[1], p[2], 2, 3, 100, 400, 100, 300, 100, 0,
+                              0, p[3], p[4], None) == 1, i
+
+
 def _backward(B=2, N=3, V=100, sb=300, sn=100, dtype=0, null=None, out=FAKE):
     p = [FAKE] * 5
     if null is not None:
@@ -78,6 +98,7 @@ def test_clip_grads_validates():
     assert _clip([good], max_norm=float("nan")) == 1
     assert _clip([good], norm=None) == 1
     assert _clip([good], n=-1) == 1
+    assert _clip([good], norm=FAKE + 2) == 1
     assert _clip([good], null=True) == 1
     for bad in ((0, FAKE, 10, 0), (FAKE, 0, 10, 0), (FAKE, FAKE, -1, 0), (FAKE, FAKE, 10, 2),
                 (FAKE + 2, FAKE, 10, 0), (FAKE, FAKE + 1, 10, 1), (FAKE, FAKE, 1 << 61, 0)):
