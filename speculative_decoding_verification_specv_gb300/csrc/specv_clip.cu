@@ -10,8 +10,9 @@
 // sums squares, in fp32 within a thread's share of a chunk (two interleaved sums of
 // up to 16 terms) and without further rounding beyond; every CTA writes its sum.  Every CTA of the
 // second launch adds those sums in the same order, so that all hold the same norm
-// (no atomics, one result), and scales its chunks, the last ones first: these the
-// first launch has left in L2, which the results, stored as streaming data, do not
+// (no atomics, one result), and scales the chunks that the CTA of its number has
+// summed, the last ones first (2.2 GB: 1037 us a call, with the chunks dealt from the
+// end 1071): these the first launch has left in L2, which the results, stored as streaming data, do not
 // push out.  The second launch begins while the first drains
 // (programmatic dependent launch).  Gradients of a call travel in the launches'
 // parameters, so nothing is copied to the device first.
@@ -231,7 +232,9 @@ __global__ void __launch_bounds__(kNT, kClipCtasPerSm)
   // a norm that is not finite gives no factor: the values are left as they are
   const float c = norm < INFINITY ? fminf(1.0f, a.max_norm / (norm + kClipEps)) : 1.0f;
   if (c == 1.0f && a.in_place) return;
-  for (int64_t j = a.chunks - 1 - blockIdx.x; j >= 0; j -= gridDim.x) {
+  // the chunks that this CTA's number has summed, the last one first
+  const int64_t mine = (a.chunks - 1 - blockIdx.x) / gridDim.x;
+  for (int64_t j = blockIdx.x + mine * gridDim.x; j >= 0; j -= gridDim.x) {
     const int k = (int)j, t = find_tensor(a, k);
     if (c == 1.0f && a.out[t] == a.in[t]) continue;
     if (a.bf16[t])
