@@ -12,15 +12,15 @@
 // Long rows.  S CTAs (a cluster) share a pair, each the same run of both rows, cut
 // into chunks of 4 KB per row.  An issuing warp brings the chunks into shared memory
 // with bulk copies, six or four of them ahead of the 128 consuming threads; after pass
-// 1 these last ones are still there for pass 2, the others are copied again, nearly all
-// from L2 (1.02 of the rows' bytes leave DRAM).  Between the passes every warp sends
+// 1 these last ones are still there for pass 2, the others are copied again, most of
+// them from L2 (1.2 of the rows' bytes leave DRAM).  Between the passes every warp sends
 // its partial sums to every CTA of the cluster, and each warp merges all of them: one
 // cluster barrier.  Rows that lie off the 16-byte boundaries are joined from whole
 // vectors as they are read from shared memory.
 //
 // What bounds it.  2048 pairs of 128256 fp32 entries take 541 us (3.15 GB, 5.8 TB/s,
-// 0.86 of the copy peak), 1024 of bf16 155 us (0.79 GB, 5.1 TB/s).  The warps issue 0.46
-// (fp32) and 0.67 (bf16) of the time, at four exponentials and some thirty instructions
+// 0.86 of the copy peak), 1024 of bf16 155 us (0.79 GB, 5.1 TB/s).  The warps issue 0.51
+// (fp32) and 0.74 (bf16) of the time, at four exponentials and some thirty instructions
 // per entry pair.  Of a CTA's time at 2048 fp32 pairs 13 % go by until its first chunk
 // is there, 38 % in pass 1, 18 % in the cluster barrier, 28 % in pass 2 (clock stamps,
 // four CTAs per SM), which the other CTAs of the SM cover only in part.  Tried and not
