@@ -532,7 +532,8 @@ typedef enum {
  * masks (-inf) makes the loss +inf (certain where its leading logit lies within 87
  * of the row's largest, open down to 175 below it); the forward gradient
  * weight * (q - p_t) is still written, the reverse gradient is NaN at every entry
- * of positive q.  A
+ * of positive q.  Finite logits may lie as far apart as their type reaches (a mask of
+ * its lowest value in one row): the divergence is then the finite one of the formula.  A
  * pair in which either row masks every entry has no divergence: loss 0, gradient
  * 0.  A NaN or +inf logit gives NaN for its pair.  Sums are fp32; a loss below
  * zero by rounding is written as 0.  (A copy into shared memory that does not land

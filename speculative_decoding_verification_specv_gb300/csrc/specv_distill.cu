@@ -45,18 +45,28 @@ namespace {
 
 constexpr float kLazy = 8.0f;   // what a term may exceed its reference by, as a power of e
 
+// Logits may lie as far apart as their type reaches (a mask of its lowest value in one
+// row of a pair only), and T adds such a distance for every entry of the run with up to
+// e^kLazy times it.  Distances are therefore held times kSmall where they go into T: a
+// power of two, so that nothing else is rounded differently, and T stays below 2^128 with
+// 2^31 entries.  Only distances below 2^-82 lose bits.
+constexpr float kLarge = 17592186044416.0f;  // 2^44
+constexpr float kSmall = 1.0f / kLarge;
+
 // Partial sums of a row pair about the references (rt, rq).
 struct PairSums {
   float rt = -3.402823466e38f, rq = -3.402823466e38f;
-  float st = 0.0f, sq = 0.0f, t = 0.0f;
+  float st = 0.0f, sq = 0.0f;
+  float t = 0.0f;  // T times kSmall
 };
 
 // The same sums about references (Mt, Mq), not below the old ones where a row has
-// entries.  REVERSE: the draft row leads.
+// entries.  REVERSE: the draft row leads.  The leading row's move scales T, both rows'
+// moves enter it as they are: the other row's may be any distance.
 template <bool REVERSE>
 __device__ __forceinline__ void move_to(PairSums &x, float Mt, float Mq) {
-  const float dt = fmaxf(__fsub_rn(x.rt, Mt), kFarBelow), dq = fmaxf(__fsub_rn(x.rq, Mq), kFarBelow);
-  const float ft = ex2(__fmul_rn(dt, kLog2e)), fq = ex2(__fmul_rn(dq, kLog2e));
+  const float dt = __fmaf_rn(x.rt, kSmall, -Mt * kSmall), dq = __fmaf_rn(x.rq, kSmall, -Mq * kSmall);
+  const float ft = ex2(__fmul_rn(dt, kLog2e * kLarge)), fq = ex2(__fmul_rn(dq, kLog2e * kLarge));
   const float lead = REVERSE ? x.sq : x.st, f = REVERSE ? fq : ft;
   // (a sum that vanishes takes an infinite one of its terms with it)
   x.t = lead == 0.0f || f == 0.0f
@@ -104,7 +114,7 @@ __device__ __forceinline__ Merged merged(const PairSums &y) {
   m.lq = log2_of(y.sq);
   m.rt = y.rt;
   m.rq = y.rq;
-  const float mean = __fdividef(y.t, REVERSE ? y.sq : y.st);
+  const float mean = __fmul_rn(__fdividef(y.t, REVERSE ? y.sq : y.st), kLarge);
   const float kl = __fmaf_rn(REVERSE ? m.lt - m.lq : m.lq - m.lt, kLn2, mean);
   m.kl = bad ? quiet_nan() : kl < 0.0f ? 0.0f : kl;
   return m;
@@ -149,13 +159,15 @@ __device__ __forceinline__ void fold_pair(PairSums &x, const TileT &xt, const Ti
   const float mt = xt.largest(), mq = xq.largest();
   if (mt > x.rt + kLazy || mq > x.rq + kLazy)
     move_to<REVERSE>(x, fmaxf(x.rt, mt), fmaxf(x.rq, mq));
-  const uint64_t nt = pack2(-x.rt, -x.rt), nq = pack2(-x.rq, -x.rq);
-  const uint64_t scale = pack2(kLog2e, kLog2e), minus = pack2(-1.0f, -1.0f);
+  const float rt = -x.rt * kSmall, rq = -x.rq * kSmall;
+  const uint64_t nt = pack2(rt, rt), nq = pack2(rq, rq);
+  const uint64_t small = pack2(kSmall, kSmall), minus = pack2(-1.0f, -1.0f);
+  const uint64_t scale = pack2(kLog2e * kLarge, kLog2e * kLarge);
   uint64_t st = 0, sq = 0;
   float t0 = 0.0f, t1 = 0.0f;
 #pragma unroll
   for (int i = 0; i < TileT::kPairs; ++i) {
-    const uint64_t dt = add2(xt.pair(i), nt), dq = add2(xq.pair(i), nq);
+    const uint64_t dt = fma2(xt.pair(i), small, nt), dq = fma2(xq.pair(i), small, nq);
     float a0, a1, b0, b1, d0, d1;
     unpack2(mul2(dt, scale), a0, a1);
     unpack2(mul2(dq, scale), b0, b1);
@@ -180,20 +192,31 @@ __device__ __forceinline__ void fold_pair(PairSums &x, const TileT &xt, const Ti
   x.t += t0 + t1;
 }
 
-// What the gradient needs of a row pair, in packed pairs.
+// What the gradient needs of a row pair, in packed pairs.  The reverse gradient is a
+// product of q and a distance: q is held times 2^kGradShift and distances divided by it, so
+// that a q just below the smallest normal number times a large distance is not lost, and
+// the distance of two entries anywhere in fp32's range is finite.  (16: the exponents of
+// the entries that matter, -20 to 0, stay small numbers and lose no bits to the shift.)
+constexpr int kGradShift = 16;
+template <bool REVERSE>
 struct GradTerms {
+  // (reverse: distances in units of 2^kGradShift)
+  static constexpr float kUnit = REVERSE ? 1.0f / (1 << kGradShift) : 1.0f;
   uint64_t rt, rq;  // -r
-  uint64_t lt, lq;  // -log2 S
+  uint64_t lt, lq;  // -log2 (kUnit S)
   uint64_t w, c;
   bool bad;
   __device__ __forceinline__ GradTerms(const Merged &m, float weight) {
+    constexpr float unit = kUnit, log2_unit = REVERSE ? kGradShift : 0.0f;
     bad = m.kl != m.kl;
     const float wg = bad ? quiet_nan() : weight;
-    const float cc = m.kl == INFINITY ? quiet_nan() : (m.lt - m.lq) * kLn2 - m.kl;
-    rt = pack2(-m.rt, -m.rt);
-    rq = pack2(-m.rq, -m.rq);
-    lt = pack2(-m.lt, -m.lt);
-    lq = pack2(-m.lq, -m.lq);
+    const float cc = m.kl == INFINITY ? quiet_nan() : ((m.lt - m.lq) * kLn2 - m.kl) * unit;
+    const float ft = -m.rt * unit, fq = -m.rq * unit;
+    const float et = log2_unit - m.lt, eq = log2_unit - m.lq;
+    rt = pack2(ft, ft);
+    rq = pack2(fq, fq);
+    lt = pack2(et, et);
+    lq = pack2(eq, eq);
     w = pack2(wg, wg);
     c = pack2(cc, cc);
   }
@@ -201,17 +224,20 @@ struct GradTerms {
 
 // Puts the gradient of the entries of xt and xq into xq.
 template <typename T, bool REVERSE, typename TileT>
-__device__ __forceinline__ void gradient(const GradTerms &g, const TileT &xt, TileT &xq) {
-  const uint64_t scale = pack2(kLog2e, kLog2e), minus = pack2(-1.0f, -1.0f);
+__device__ __forceinline__ void gradient(const GradTerms<REVERSE> &g, const TileT &xt, TileT &xq) {
+  constexpr float kUnit = GradTerms<REVERSE>::kUnit, kScale = kLog2e / kUnit;
+  const uint64_t scale = pack2(kScale, kScale), minus = pack2(-1.0f, -1.0f);
+  const uint64_t unit = pack2(kUnit, kUnit);
 #pragma unroll
   for (int i = 0; i < TileT::kPairs; ++i) {
-    const uint64_t dt = add2(xt.pair(i), g.rt), dq = add2(xq.pair(i), g.rq);
+    const uint64_t dt = REVERSE ? fma2(xt.pair(i), unit, g.rt) : add2(xt.pair(i), g.rt);
+    const uint64_t dq = REVERSE ? fma2(xq.pair(i), unit, g.rq) : add2(xq.pair(i), g.rq);
     float q0, q1, g0, g1;
     unpack2(fma2(dq, scale, g.lq), q0, q1);
     q0 = ex2(q0);
     q1 = ex2(q1);
     if (REVERSE) {
-      unpack2(mul2(mul2(g.w, pack2(q0, q1)), add2(fma2(dt, minus, dq), g.c)), g0, g1);
+      unpack2(mul2(g.w, mul2(pack2(q0, q1), add2(fma2(dt, minus, dq), g.c))), g0, g1);
       if (q0 == 0.0f) g0 = 0.0f;
       if (q1 == 0.0f) g1 = 0.0f;
       if (g.bad) g0 = g1 = quiet_nan();
@@ -277,7 +303,7 @@ __global__ void __launch_bounds__(kShortNT, 4) distill_short_kernel(DistillArgs 
   }
   if (lane == 0) a.out_loss[r] = w * m.kl;
   if (out == nullptr) return;
-  gradient<T, REVERSE>(GradTerms(m, w), xt, xq);
+  gradient<T, REVERSE>(GradTerms<REVERSE>(m, w), xt, xq);
   store();
 }
 
@@ -532,7 +558,7 @@ __global__ void __launch_bounds__(kNT + 32, MIN_CTAS) distill_kernel(DistillArgs
   }
 
   // ----------------------------------------------------------- pass 2: the gradient
-  GradTerms g(m, w);
+  GradTerms<REVERSE> g(m, w);
   for (int c = n - 1; c >= 0; --c) {
     const bool inner = is_inner(c);
     take(c, load_2(c), c < n - kBuffers, inner);
