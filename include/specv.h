@@ -34,7 +34,9 @@
  *     host-buffer calls' staging (see specv_verify_host), one per (device, stream):
  *     created on the first call on that stream that needs it, reused by
  *     every later call on the stream (calls on one stream are ordered, so
- *     they never overlap), kept until the process exits.  A call made while
+ *     they never overlap; host threads that call on one stream take turns, so
+ *     that nothing comes between the launches of a call that leave and read
+ *     data there), kept until the process exits.  A call made while
  *     `stream` is being captured into a CUDA graph uses the stream's existing
  *     workspace (the graph then refers to it: replay such a graph only where
  *     it cannot overlap other calls on that stream); if there is none yet it

@@ -80,6 +80,10 @@ struct Workspace {
   std::vector<void *> superseded;
 };
 std::vector<Workspace> g_ws;
+// The turns of calls that use a stream's scratch, streams dealt over a fixed number of
+// locks (two streams that share one only wait for each other's launches).
+constexpr size_t kTurns = 64;
+std::mutex g_turn[kTurns];
 constexpr size_t kWsMinBytes = 64 * 1024;
 
 size_t grow_to(size_t need) {
@@ -146,6 +150,7 @@ bool cached_workspace(int dev, cudaStream_t stream, int64_t B, size_t data_bytes
 }
 
 using specv::note_cuda_error;
+using specv::stream_turn;
 
 // One-time per-device set-up: opt the kernels into 16-CTA clusters and the
 // tile kernel into its shared-memory size; read the SM count.
@@ -522,6 +527,7 @@ specv_status run(const void *target, const void *draft, const int32_t *tokens, c
   void *wdata = nullptr;
   void *ws = nullptr;
   e = cudaSuccess;
+  const auto turn = stream_turn(stream);
   const bool per_call = !cached_workspace(dev, stream, p.counters, data_bytes, &cnt, &wdata);
   if (per_call) {
     e = cudaMallocAsync(&ws, (size_t)p.ws_bytes, stream);
@@ -1225,6 +1231,11 @@ namespace specv {
 
 int device_ready(int *sms) { return ensure_device(sms, nullptr); }
 
+std::unique_lock<std::mutex> stream_turn(cudaStream_t stream) {
+  const uint64_t h = reinterpret_cast<uint64_t>(stream) * 0x9e3779b97f4a7c15ull;
+  return std::unique_lock<std::mutex>(g_turn[h >> 58]);  // the top 6 bits: 0 .. kTurns-1
+}
+
 bool stream_scratch(cudaStream_t stream, size_t bytes, void **data) {
   int dev = 0;
   unsigned *count = nullptr;
@@ -1407,6 +1418,7 @@ specv_status specv_verify_tree(const void *target_logits, const void *draft_logi
   void *wdata = nullptr;
   void *ws = nullptr;
   cudaError_t e = cudaSuccess;
+  const auto turn = stream_turn(s);
   const bool per_call = !cached_workspace(dev, s, B, data_bytes, &cnt, &wdata);
   if (per_call) {
     e = cudaMallocAsync(&ws, data_bytes + (size_t)round16(B * 4), s);
@@ -1546,6 +1558,7 @@ specv_status specv_release_stream(void *stream) {
     return SPECV_ERR_CUDA;
   }
   if (cap != cudaStreamCaptureStatusNone) return SPECV_ERR_UNSUPPORTED;
+  const auto turn = stream_turn(s);  // no call is between its scratch and its launches
   std::vector<void *> dev_bufs, host_bufs;
   std::vector<cudaStream_t> copy_streams;
   std::vector<cudaEvent_t> events;

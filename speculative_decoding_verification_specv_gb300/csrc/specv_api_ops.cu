@@ -3,6 +3,7 @@
 //
 // Host-side work only: argument validation, launch shapes, the launches.
 #include <cstdint>
+#include <mutex>
 
 #include <nvtx3/nvToolsExt.h>
 
@@ -237,7 +238,9 @@ specv_status specv_clip_grads(const specv_grad *grads, int64_t n, float max_norm
   void *scratch = nullptr;
   const size_t bytes = sizeof(float2) * specv::kClipPartials;
   bool cached = false;
+  std::unique_lock<std::mutex> turn;  // the second launch reads what the first one leaves
   try {
+    turn = specv::stream_turn(st);
     cached = specv::stream_scratch(st, bytes, &scratch);
   } catch (...) {
     return SPECV_ERR_NO_MEMORY;

@@ -2,6 +2,8 @@
 #pragma once
 
 #include <cstdint>
+#include <mutex>
+
 #include <cuda_runtime.h>
 
 namespace specv {
@@ -15,7 +17,11 @@ void note_cuda_error(cudaError_t e);
 // device's SM count.  stream_scratch: the stream's cached scratch with room for
 // `bytes` bytes, or false (the caller then takes stream-ordered memory).
 // cluster_override: SPECV_CLUSTER_SIZE, 0 if unset.
+// stream_turn: held from asking for a stream's scratch to the last launch that uses it,
+// so that calls of several host threads on one stream do not come between one another's
+// launches.
 int device_ready(int *sms);
+std::unique_lock<std::mutex> stream_turn(cudaStream_t stream);
 bool stream_scratch(cudaStream_t stream, size_t bytes, void **data);
 int cluster_override();
 
