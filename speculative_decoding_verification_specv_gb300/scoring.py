@@ -47,6 +47,14 @@ def _entry(name: str):
     return fn
 
 
+def _elsewhere(stream, dev):
+    """The context that a call on tensors of ``dev`` is to be made in: None where that is
+    the current device (the library launches on it, and takes its scratch there)."""
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream must be of {dev}, got {stream.device}")
+    return None if dev.index == torch._C._cuda_getDevice() else torch.cuda.device(dev)
+
+
 def _stream(stream, dev) -> int:
     if stream is not None:
         return stream.cuda_stream
@@ -97,6 +105,10 @@ def token_logprobs(logits, tokens, top_n: int = 0, stream=None) -> TokenLogprobs
     n = int(top_n)
     if not 0 <= n <= MAX_TOP:
         raise ValueError(f"top_n must be in 0..{MAX_TOP}")
+    there = _elsewhere(stream, dev)
+    if there is not None:
+        with there:
+            return token_logprobs(logits, tokens, n, stream)
     logprobs = _empty(lead, dtype=_f32, device=dev)
     entropy = _empty(lead, dtype=_f32, device=dev)
     stats = _empty((*lead, 2), dtype=_f32, device=dev)
@@ -132,10 +144,15 @@ def token_logprobs_backward(logits, tokens, stats, entropy, grad_logprobs, grad_
     _fit(grad_logprobs, "grad_logprobs", _f32, lead, dev)
     if grad_entropy is not None:
         _fit(grad_entropy, "grad_entropy", _f32, lead, dev)
+    if out is not None:
+        _fit(out, "out", logits.dtype, logits.shape, dev)
+    there = _elsewhere(stream, dev)
+    if there is not None:
+        with there:
+            return token_logprobs_backward(logits, tokens, stats, entropy, grad_logprobs,
+                                           grad_entropy, out, stream)
     if out is None:
         out = _empty(logits.shape, dtype=logits.dtype, device=dev)
-    else:
-        _fit(out, "out", logits.dtype, logits.shape, dev)
     st = _entry("specv_token_logprobs_backward")(
         logits.data_ptr(), tokens.data_ptr(), stats.data_ptr(), entropy.data_ptr(),
         grad_logprobs.data_ptr(), None if grad_entropy is None else grad_entropy.data_ptr(), B, N,
@@ -174,10 +191,14 @@ def distill(target_logits, draft_logits, weight=None, kind: int = FORWARD_KL, ne
         _fit(weight, "weight", torch.float32, (B, K), dev)
     if kind not in (FORWARD_KL, REVERSE_KL):
         raise ValueError("kind must be FORWARD_KL (0) or REVERSE_KL (1)")
-    loss = _empty((B, K), dtype=_f32, device=dev)
     if out_grad is not None:
         _fit(out_grad, "out_grad", draft_logits.dtype, (B, K, V), dev)
-    elif need_grad:
+    there = _elsewhere(stream, dev)
+    if there is not None:
+        with there:
+            return distill(target_logits, draft_logits, weight, kind, need_grad, out_grad, stream)
+    loss = _empty((B, K), dtype=_f32, device=dev)
+    if out_grad is None and need_grad:
         out_grad = _empty((B, K, V), dtype=draft_logits.dtype, device=dev)
     st = _entry("specv_distill")(
         target_logits.data_ptr(), draft_logits.data_ptr(),
@@ -207,7 +228,12 @@ def clip_grads(grads, max_norm: float, out=None, stream=None) -> torch.Tensor:
     if not max_norm >= 0.0:
         raise ValueError("max_norm must be >= 0")
     at, counts, codes = _table(grads, "gradient")
-    dev = grads[0].device if grads else torch.device("cuda", torch.cuda.current_device())
+    if grads:
+        dev = grads[0].device
+    elif stream is not None:
+        dev = stream.device
+    else:
+        dev = torch.device("cuda", torch.cuda.current_device())
     if out is grads:
         to = at
     else:
@@ -217,6 +243,10 @@ def clip_grads(grads, max_norm: float, out=None, stream=None) -> torch.Tensor:
     live = [p for p, n in zip(at, counts) if n]
     if len(set(live)) != len(live):
         raise ValueError("a gradient is listed twice")
+    there = _elsewhere(stream, dev)
+    if there is not None:
+        with there:
+            return clip_grads(grads, max_norm, None if out is grads else out, stream)
     table = array("q", bytes(32 * len(grads)))
     table[0::4], table[1::4] = array("q", at), array("q", to)
     table[2::4], table[3::4] = array("q", counts), array("q", codes)
