@@ -48,16 +48,20 @@ def _entry(name: str):
 
 
 def _elsewhere(stream, dev):
-    """The context that a call on tensors of ``dev`` is to be made in: None where that is
-    the current device (the library launches on it, and takes its scratch there)."""
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"stream must be of {dev}, got {stream.device}")
+    """The context that a call on tensors of ``dev`` is to be made in, or None.
+
+    Where ``dev`` is not current it becomes so (the library launches on the current
+    device, and takes its scratch there).  A given stream becomes the current one, so
+    that the results are allocated on it too: memory of another stream could still be in
+    use there when the kernel writes it, or be given away there before the kernel has."""
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream must be of {dev}, got {stream.device}")
+        return torch.cuda.stream(stream)
     return None if dev.index == torch._C._cuda_getDevice() else torch.cuda.device(dev)
 
 
-def _stream(stream, dev) -> int:
-    if stream is not None:
-        return stream.cuda_stream
+def _stream(dev) -> int:
     return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
@@ -96,7 +100,7 @@ def token_logprobs(logits, tokens, top_n: int = 0, stream=None) -> TokenLogprobs
     lower token; masked (-inf) entries are none.  Rows with a NaN or +inf, or with
     a token outside [0, V), give NaN; rows that mask every entry a log probability
     of -inf and an entropy of 0.  Asynchronous on ``stream`` (default: the current
-    stream).  No autograd graph is recorded: token_logprobs_backward is the gradient.
+    stream), on which the results are allocated.  No autograd graph is recorded: token_logprobs_backward is the gradient.
     """
     B, N, V, sb, sn = _rows(logits, "logits")
     dev, lead = logits.device, logits.shape[:-1]
@@ -108,7 +112,7 @@ def token_logprobs(logits, tokens, top_n: int = 0, stream=None) -> TokenLogprobs
     there = _elsewhere(stream, dev)
     if there is not None:
         with there:
-            return token_logprobs(logits, tokens, n, stream)
+            return token_logprobs(logits, tokens, n)
     logprobs = _empty(lead, dtype=_f32, device=dev)
     entropy = _empty(lead, dtype=_f32, device=dev)
     stats = _empty((*lead, 2), dtype=_f32, device=dev)
@@ -119,7 +123,7 @@ def token_logprobs(logits, tokens, top_n: int = 0, stream=None) -> TokenLogprobs
     st = _entry("specv_token_logprobs")(
         logits.data_ptr(), tokens.data_ptr(), B, N, V, sb, sn, code, n, logprobs.data_ptr(),
         entropy.data_ptr(), stats.data_ptr(), top_t.data_ptr() if n else None,
-        top_l.data_ptr() if n else None, _stream(stream, dev))
+        top_l.data_ptr() if n else None, _stream(dev))
     if st:
         _check(st, "specv_token_logprobs")
     return TokenLogprobs(logprobs, entropy, stats, top_t, top_l)
@@ -150,13 +154,13 @@ def token_logprobs_backward(logits, tokens, stats, entropy, grad_logprobs, grad_
     if there is not None:
         with there:
             return token_logprobs_backward(logits, tokens, stats, entropy, grad_logprobs,
-                                           grad_entropy, out, stream)
+                                           grad_entropy, out)
     if out is None:
         out = _empty(logits.shape, dtype=logits.dtype, device=dev)
     st = _entry("specv_token_logprobs_backward")(
         logits.data_ptr(), tokens.data_ptr(), stats.data_ptr(), entropy.data_ptr(),
         grad_logprobs.data_ptr(), None if grad_entropy is None else grad_entropy.data_ptr(), B, N,
-        V, sb, sn, code, out.data_ptr(), _stream(stream, dev))
+        V, sb, sn, code, out.data_ptr(), _stream(dev))
     if st:
         _check(st, "specv_token_logprobs_backward")
     return out
@@ -196,7 +200,7 @@ def distill(target_logits, draft_logits, weight=None, kind: int = FORWARD_KL, ne
     there = _elsewhere(stream, dev)
     if there is not None:
         with there:
-            return distill(target_logits, draft_logits, weight, kind, need_grad, out_grad, stream)
+            return distill(target_logits, draft_logits, weight, kind, need_grad, out_grad)
     loss = _empty((B, K), dtype=_f32, device=dev)
     if out_grad is None and need_grad:
         out_grad = _empty((B, K, V), dtype=draft_logits.dtype, device=dev)
@@ -204,7 +208,7 @@ def distill(target_logits, draft_logits, weight=None, kind: int = FORWARD_KL, ne
         target_logits.data_ptr(), draft_logits.data_ptr(),
         None if weight is None else weight.data_ptr(), B, K, V, tsb, tsk, dsb, dsk, code,
         int(kind), loss.data_ptr(), None if out_grad is None else out_grad.data_ptr(),
-        _stream(stream, dev))
+        _stream(dev))
     if st:
         _check(st, "specv_distill")
     return loss, out_grad
@@ -246,13 +250,13 @@ def clip_grads(grads, max_norm: float, out=None, stream=None) -> torch.Tensor:
     there = _elsewhere(stream, dev)
     if there is not None:
         with there:
-            return clip_grads(grads, max_norm, None if out is grads else out, stream)
+            return clip_grads(grads, max_norm, None if out is grads else out)
     table = array("q", bytes(32 * len(grads)))
     table[0::4], table[1::4] = array("q", at), array("q", to)
     table[2::4], table[3::4] = array("q", counts), array("q", codes)
     norm = _empty((), dtype=_f32, device=dev)
     st = _entry("specv_clip_grads")(table.buffer_info()[0] if grads else None, len(grads), max_norm,
-                                    norm.data_ptr(), _stream(stream, dev))
+                                    norm.data_ptr(), _stream(dev))
     if st:
         _check(st, "specv_clip_grads")
     return norm
