@@ -572,7 +572,8 @@ typedef struct {
  * finite leaves the values as they are (copied when out differs from grad), so
  * that a training loop can look at the norm and drop the step.  Squares are
  * summed in fp32 within 32 elements and to fp64 precision beyond, in a fixed order; an
- * element beyond 1.8e19 overflows its square and with it the norm.  No element
+ * element beyond 1.8e19 overflows its square and with it the norm, one below 1e-19
+ * loses bits of its square, one below 2.6e-23 adds nothing.  No element
  * may be listed twice.  Scratch: at most 64 KiB in the stream's workspace (see
  * specv_verify).  Asynchronous on `stream`.
  */

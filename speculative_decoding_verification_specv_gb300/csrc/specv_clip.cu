@@ -12,12 +12,12 @@
 // the second launch adds those sums in the same order, so that all hold the same norm
 // (no atomics, one result), and scales the chunks that the CTA of its number has
 // summed, the last ones first: those the first launch has left in L2, which the
-// results, stored as streaming data, do not push out (2.2 GB: 1037 us a call; with
+// results, stored as streaming data, do not push out (2.2 GB: 1040 us a call; with
 // the chunks dealt from the end 1071, with ordinary stores 1120).  The second launch
 // begins while the first drains (programmatic dependent launch).  The gradients of a
 // call travel in the launches' parameters: nothing is copied to the device first.
 // Bound by HBM for large sets (two reads and a write: 976 us for the 2.2 GB), by the
-// two launches for small ones (16 MB: 6.0 us).
+// two launches for small ones (16 MB: 6.0 to 6.4 us).
 #include "specv_internal.h"
 #include "specv_rowstat.cuh"
 

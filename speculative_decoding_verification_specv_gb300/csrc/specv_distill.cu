@@ -18,9 +18,10 @@
 // cluster barrier.  Rows that lie off the 16-byte boundaries are joined from whole
 // vectors as they are read from shared memory.
 //
-// What bounds it.  2048 pairs of 128256 fp32 entries take 541 us (3.15 GB, 5.8 TB/s,
-// 0.86 of the copy peak), 1024 of bf16 155 us (0.79 GB, 5.1 TB/s).  The warps issue 0.51
-// (fp32) and 0.74 (bf16) of the time, at four exponentials and some thirty instructions
+// What bounds it.  2048 pairs of 128256 fp32 entries take 545 us (3.15 GB, 5.8 TB/s,
+// 0.85 of the copy peak), 1024 of bf16 155 us (0.79 GB, 5.1 TB/s); the loss alone, one
+// pass, 298 us (7.1 TB/s) and 87 (6.0).  The warps issue 0.51
+// (fp32) and 0.73 (bf16) of the time, at four exponentials and some thirty instructions
 // per entry pair.  Of a CTA's time at 2048 fp32 pairs 13 % go by until its first chunk
 // is there, 38 % in pass 1, 18 % in the cluster barrier, 28 % in pass 2 (clock stamps,
 // four CTAs per SM), which the other CTAs of the SM cover only in part.  Tried and not
@@ -255,7 +256,8 @@ __device__ __forceinline__ void gradient(const GradTerms<REVERSE> &g, const Tile
 constexpr int kShortNT = 128;
 constexpr int kShortPacks = 8;  // U at most: pairs of 2048 bf16 or 1024 fp32 entries
 
-// (four CTAs per SM: 12495 pairs of 1513 bf16 entries 40 us, with 165 registers 56)
+// (four CTAs per SM: 12495 pairs of 1513 bf16 entries, half of them left out, 39 us, with
+// the registers it would take otherwise 42; with none left out 46 both)
 template <typename T, bool SHIFTED, bool REVERSE, int U>
 __global__ void __launch_bounds__(kShortNT, 4) distill_short_kernel(DistillArgs a) {
   const int lane = threadIdx.x & 31;
@@ -616,9 +618,9 @@ cudaError_t plan(const DistillArgs &a, int sms, int S, cudaStream_t stream) {
   }
   // CTAs per pair: so many that each takes 4096 packs of a row at most, more while one
   // wave of 4 CTAs per SM has room for them, 8 at most.  More CTAs hold more of the pair
-  // but wait longer for one another.  Measured, us: 2048 pairs of 32064 packs S = 8 565,
-  // 6 614, 4 667; 1024 of 16032 S = 4 164, 8 177, 2 182; 396 of 9760 S = 3 48, 6 53, 1 55;
-  // 1776 of 3019 S = 1 55, 2 64; 34 of 14540 S = 8 11.6, 4 16, 2 28.
+  // but wait longer for one another.  Measured, us: 2048 pairs of 32064 packs S = 8 544,
+  // 6 595, 4 663; 1024 of 16032 S = 4 155, 8 158, 2 178; 396 of 9760 S = 3 47, 1 46, 8 48;
+  // 1776 of 3019 S = 1 48, 2 54; 34 of 14540 S = 8 9.0, 4 11.9, 2 20.7.
   if (S == 0) {
     const int64_t pairs = a.B * a.K;
     S = (int)std::min<int64_t>((packs + 4095) / 4096, 8);
@@ -628,9 +630,9 @@ cudaError_t plan(const DistillArgs &a, int sms, int S, cudaStream_t stream) {
   while (S > 1 && a.B * a.K * S > INT32_MAX) S /= 2;
   // Six chunks held and four CTAs per SM where that is one wave, else four and six: a
   // full GPU gains more from CTAs than from what they hold.  Us, six held and four: 1024
-  // pairs of 16032 packs 161 and 155, 2048 of 32064 560 and 550, 880 of 3429 (joined)
-  // 48.5 and 43.4, 9207 of 1140 127 and 116; 133 of 6251 (joined) 16.3 and 17.5, 24 of
-  // 12545 8.7 and 9.7.
+  // pairs of 16032 packs 159 and 155, 2048 of 32064 555 and 544, 880 of 3429 (joined)
+  // 48.0 and 43.0, 9207 of 1140 96 and 88; 133 of 6251 (joined) 15.8 and 16.9, 24 of
+  // 12545 8.1 and 8.7.
   if (a.B * a.K * S <= 4 * sms) return launch_long<T, SHIFTED, REVERSE, 6, 4>(a, S, stream);
   return launch_long<T, SHIFTED, REVERSE, 4, 6>(a, S, stream);
 }

@@ -26,9 +26,12 @@
 // a repeated search instead, whose result is the same.
 //
 // What bounds it.  2304 rows of 128256 fp32 entries take 184 us (1.18 GB, 6.4 TB/s, 0.95
-// of the copy peak) with one alternative, 174 with none, 199 with 20; in bf16 102 us
-// with none (0.59 GB, 5.8 TB/s: nine instructions per entry).  Few rows are bound by
-// latency: nine rows of 128256 bf16 entries 6.9 us, five alternatives.
+// of the copy peak) with one alternative, 175 with none, 199 with 20; in bf16 102 us
+// with none (0.59 GB, 5.8 TB/s: nine instructions per entry), 110 with one, 124 with 20.
+// Few rows are bound by latency: nine rows of 128256 bf16 entries 7.0 us, five
+// alternatives.  Rows of some thousand entries are bound by what a row costs whatever its
+// length, a batch of the streaming loop and the selection: 30000 of 2500 fp32 entries
+// (0.3 GB) 129 us with no alternatives, 227 with five.
 #include <algorithm>
 
 #include <cooperative_groups.h>
@@ -354,12 +357,13 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 1024 / NT)
 // ------------------------------------------------------------------ the gradient
 //   dz_v = g (1[v = x] - p_v) - h p_v (ln p_v + H)
 // from the statistics of the forward pass: each entry is read and its gradient
-// written once, at the copy rate (2048 rows of 128256 bf16 entries 147 us, 6.8 TB/s).  A warp takes some packs per lane of one row, on the grid of
+// written once, at the copy rate (2048 rows of 128256 bf16 entries, a tenth of them without
+// a token, 147 us, 6.8 TB/s).  A warp takes some packs per lane of one row, on the grid of
 // the output's row.
 constexpr int kGradNT = 256;
 // Packs per lane: 8 in flight for aligned rows; rows to be joined keep 4 (their
-// registers).  2048 rows of 128256 bf16 entries: 144 us with 8, 151 with 4, 162 with 2;
-// 2349 rows of 14957 in a padded buffer: 25 us with 4, 30 with 8.
+// registers).  The 2048 rows above: 147 us with 8, 146 with 4, 162 with 2; 2349 rows of
+// 14957 bf16 entries in a padded buffer: 29 us with 4, 35 with 8.
 template <bool SHIFTED>
 constexpr int kGradUnroll = SHIFTED ? 4 : 8;
 template <bool SHIFTED>
@@ -462,9 +466,13 @@ cudaError_t forward(const LogprobArgs &a, int sms, int S, cudaStream_t stream) {
   while (S > 1 && a.R * S > INT32_MAX) S /= 2;
   if (S > 1) return launch_forward<T, 256, true, 1>(a, S, stream);
   // Segments, for several alternatives of long rows: what is read again of a strip,
-  // from DRAM in a batch whose rows overfill L2, is then an eighth.  2304 rows of
-  // 128256 entries, us with and without: fp32 20 alternatives 199 and 279, 5 189 and
-  // 198, 1 187 and 184; bf16 20 126 and 145, 5 117 and 116, 1 115 and 110.
+  // from DRAM in a batch whose rows overfill L2, is then an eighth.  2304 rows, us with
+  // and without: of 32064 vectors fp32 20 alternatives 199 and 279, 5 188 and 199, 4 188
+  // and 194, bf16 20 224 and 295, 5 212 and 217, 4 212 and 212; of 16032 fp32 20 110 and
+  // 134, 5 105 and 106, bf16 20 124 and 147, 5 119 and 116; of 12288 fp32 20 86 and 98, 5
+  // 82 and 79, bf16 20 97 and 108, 5 93 and 88; of 9000 fp32 20 70 and 75, 5 66 and 63.
+  // Many alternatives gain from shorter rows on than five do: near the edge the rule
+  // costs five alternatives up to 5 % and gives twenty 10 %.
   return a.top_n >= kSegTop && vectors >= kSegVectors
              ? launch_forward<T, 256, false, 8>(a, 1, stream)
              : launch_forward<T, 256, false, 1>(a, 1, stream);

@@ -448,7 +448,7 @@ struct PackTile {
 // Writes a pack of a row on its own grid: a full one as one access, an edge one
 // entry by entry.  Streaming stores: what is written is not read again here, and
 // ordinary stores took the L2 from the rows still to be read (gradient of 2048 rows of
-// 128256 bf16 entries: 168 us, streaming 151).
+// 128256 bf16 entries: 157 us, streaming 147).
 template <typename T>
 __device__ __forceinline__ void store_pack(T *row, const Grid<T> &grid, int k, const uint4 &v) {
   constexpr int VW = Elem<T>::kPerVec;
