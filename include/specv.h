@@ -614,7 +614,7 @@ typedef struct {
  *   running sum of kept weights, in index order, exceeds u W.
  *
  *   logits         element (b, n, v) at b * stride_b + n * stride_n + v (strides >= 0)
- *   u              [B][N]  fp32 in [0, 1]; at 1 the last kept entry of positive weight
+ *   u              [B][N]  fp32 in [0, 1]; at 1 the last kept entry that counts (below)
  *   params         on the HOST, read before the call returns
  *   B, N, V >= 1, B * N < 2^31
  *   out_tokens     [B][N]  int32
@@ -627,10 +627,10 @@ typedef struct {
  *                          contiguous and of the same type (in place)
  *   filtered_dtype the logits' dtype, or SPECV_F32
  *
- * Weights are fp32, the largest 1; the sums that decide (a share, a running sum) hold each to
- * about 2^-45 (V above 2^18: V 2^-63), so that the result does not depend on the launch but
- * where a border lies that close.  (The log probability of a row that nothing filters takes
- * an fp32 sum.)  A -inf logit masks its entry: it is never kept.  A row that masks every
+ * Weights are fp32, the largest 1; the sums that decide (a share, a running sum) are of whole
+ * numbers of 2^-44 (V above 2^18: of 2^-62 times the next power of two from V on), each weight
+ * rounded to one, so that the result does not depend on the launch.  A weight below half of
+ * that counts as none.  (The log probability of a row that nothing filters takes an fp32 sum.)  A -inf logit masks its entry: it is never kept.  A row that masks every
  * entry gives token -1, log probability 0 and log-normaliser -inf.  A row with a NaN or
  * +inf, a parameter outside its range or a u outside [0, 1] gives token -1 and NaN (its
  * filtered row too).  No scratch, no allocation; asynchronous on `stream`; host argument

@@ -11,9 +11,9 @@
 //          u times their sum W;  ln p = fl(fl(z - m) r) - ln W
 // T = 0 keeps the first entry of the order alone.
 //
-// Weights are added as whole numbers of 2^-44 (less for V above 2^18), or in pairs of fp32
-// that hold about as much, so a border (a prefix against u W, a mass against p W) is decided on the
-// sum of the fp32 weights and not on an order of addition.  Nothing here is fp64: its
+// Weights are added as whole numbers of 2^-44 (less for V above 2^18), so a border (a prefix
+// against u W, a mass against p W) is decided on the sum of the fp32 weights and not on an
+// order of addition, and sums of different passes agree.  Nothing here is fp64: its
 // instructions run at 1/64 of the fp32 rate, and a dozen of them in every thread of a row
 // took 6 us.
 //
@@ -233,13 +233,16 @@ __device__ __forceinline__ void run_sums(SampleShared<NT> &sh, const RowVectors<
   const int end = (int)min((int64_t)hi, (int64_t)first + per);
   uint64_t s = 0;
   if constexpr (!F::kFloor) {  // every weight
-    PairSum sum;
+    const Units units(f.p.scale);
     for_vectors<T, NT, 32>(sh, row, first, end, lane, [&](const uint4 &v, int) {
+      UnitSum sum = units.begin(Elem<T>::kPerVec), a, b;
 #pragma unroll
-      for (int e = 0; e < Elem<T>::kPerVec; e += 2)
-        sum.add(f.p.weight(Elem<T>::get(v, e)), f.p.weight(Elem<T>::get(v, e + 1)));
+      for (int e = 0; e < Elem<T>::kPerVec; e += 2) {
+        units.split(f.p.weight(Elem<T>::get(v, e)), f.p.weight(Elem<T>::get(v, e + 1)), a, b);
+        Units::add(sum, a, b);
+      }
+      s += units.total(sum);
     });
-    s = sum.units(f.p.scale);
   } else {
     for_vectors<T, NT, 32>(sh, row, first, end, lane, [&](const uint4 &v, int k) {
       s += sum_of<T>(f, v, (int)row.index(k, 0));
@@ -710,16 +713,17 @@ __device__ __noinline__ Found search_bracket() {
   };
   uint64_t above = 0, mass = 0, whole = 0;  // before the bracket: entries, weights; all weights
   if (by_mass && !q.exact) {
-    PairSum sum, sum_a;  // (nothing is cut yet)
+    const Units units(p.scale);  // (nothing is cut yet)
     for_vectors<T, NT, 32>(sh, row, begin, end, lane, [&](const uint4 &v, int k) {
       bool some = false;
+      UnitSum all = units.begin(VW), near = units.begin(VW), a, b;
 #pragma unroll
       for (int e = 0; e < VW; e += 2) {
         const float z0 = Elem<T>::get(v, e), z1 = Elem<T>::get(v, e + 1);
         const float d0 = __fsub_rn(m, z0), d1 = __fsub_rn(m, z1);
-        const float w0 = p.weight(z0), w1 = p.weight(z1);
-        sum.add(w0, w1);
-        sum_a.add(d0 < d_lo ? w0 : 0.0f, d1 < d_lo ? w1 : 0.0f);
+        units.split(p.weight(z0), p.weight(z1), a, b);
+        Units::add(all, a, b);
+        Units::add(near, d0 < d_lo ? a : units.none(), d1 < d_lo ? b : units.none());
         some |= (d0 >= d_lo && d0 < d_hi) || (d1 >= d_lo && d1 < d_hi);
       }
       if (some) {
@@ -730,9 +734,9 @@ __device__ __noinline__ Found search_bracket() {
           if (d >= d_lo && d < d_hi) list(z, at + e);
         }
       }
+      whole += units.total(all);
+      mass += units.total(near);
     });
-    whole = sum.units(p.scale);
-    mass = sum_a.units(p.scale);
   } else {
     for_vectors<T, NT, 32>(sh, row, begin, end, lane, [&](const uint4 &v, int k) {
       if (!(__fsub_rn(m, vector_max<T>(v)) < d_hi)) return;
@@ -1272,10 +1276,8 @@ __device__ __noinline__ void by_passes(const SampleArgs &a, const Rest q) {
     }
     // (close to a weight of 1 the logarithm wants the exact sum)
     if (x < 0 || q.about < 1.05f) {
-      x = draw_all<T, NT>(q.u, summed);
-      // (the cut's sums may be units off the search's: at a run's very end it finds nothing)
-      if (x < 0 && summed) x = draw_all<T, NT>(q.u, false);
-      x = max(0, x);
+      // (within the row whatever happens: a caller may write it meanwhile)
+      x = max(0, draw_all<T, NT>(q.u, summed));
       ln = ln_units(sh.before, sh.params.scale);
     }
     if (threadIdx.x == 0) {

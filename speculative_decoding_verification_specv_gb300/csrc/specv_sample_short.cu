@@ -11,7 +11,7 @@
 // Where top-k leaves 64 entries or fewer they are compared one with another instead.
 // Bound by instructions, some thousands for each row, at 16 warps per SM (128 registers):
 // 4096 rows of 1000 fp32 entries (16 MB, 2.4 us) 21 us with no filter, 33 with top-k 50, 38
-// with top-p 0.9 on top, 66 with top-p alone; a CTA of 256 threads per row took 71, 66, 72
+// with top-p 0.9 on top, 56 with top-p alone; a CTA of 256 threads per row took 71, 66, 72
 // and 89.
 #include "specv_internal.h"
 #include "specv_rowstat.cuh"
@@ -55,11 +55,14 @@ struct ShortRow {
     return __reduce_add_sync(~0u, n);
   }
   __device__ __forceinline__ uint64_t mass(float c, float scale) const {
-    PairSum sum;
+    const Units units(scale);
+    UnitSum sum = units.begin(kEach), a, b;
 #pragma unroll
-    for (int i = 0; i < kEach; i += 2)
-      sum.add(z(i) >= c ? w[i] : 0.0f, z(i + 1) >= c ? w[i + 1] : 0.0f);
-    return warp_sum_u64(sum.units(scale));
+    for (int i = 0; i < kEach; i += 2) {
+      units.split(z(i) >= c ? w[i] : 0.0f, z(i + 1) >= c ? w[i + 1] : 0.0f, a, b);
+      Units::add(sum, a, b);
+    }
+    return units.warp_total(sum);
   }
   // The index of the n-th entry (from 1) that equals c, in index order.
   __device__ __forceinline__ int nth_equal(const RowVectors<T> &row, float c, int n) const {

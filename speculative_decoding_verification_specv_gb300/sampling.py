@@ -82,8 +82,10 @@ def sample_tokens(logits, u, temperature=None, top_k=None, top_p=None, min_p=Non
     Entries are ordered by falling logits, equal ones by rising index: top_k keeps the
     first, top_p the fewest first that hold that share of what top_k keeps, min_p
     those of at least min_p times the largest probability.  The token is the first
-    kept index whose running sum exceeds u times the kept sum; weights are fp32
-    exponentials, the largest 1, and the sums that decide hold each to about 2^-45.
+    kept index whose running sum exceeds u times the kept sum (at 1 the last kept one);
+    weights are fp32 exponentials, the largest 1, each rounded to 2^-44 (V above 2^18: to
+    2^-62 times the next power of two) for the sums that decide: below half of that it
+    counts as none.
 
     With ``out_filtered`` (contiguous, of the logits' shape, float32 or the logits'
     type; may be the logits themselves) the filtered rows are written as well, as
