@@ -224,11 +224,12 @@ struct Request {
   bool bad;                  // a value outside its range
 
   __device__ __forceinline__ Request(const SampleArgs &a, int64_t row) {
-    const float T = param(a.temperature, a.temperature_all, row);
-    top_p = param(a.top_p, a.top_p_all, row);
+    // (-0 + 0 is +0: of -0 the reciprocal would be -inf, and the bits no share)
+    const float T = __fadd_rn(param(a.temperature, a.temperature_all, row), 0.0f);
+    top_p = __fadd_rn(param(a.top_p, a.top_p_all, row), 0.0f);
     top_k = param(a.top_k, a.top_k_all, row);
-    min_p = param(a.min_p, a.min_p_all, row);
-    u = a.u != nullptr ? a.u[row] : 0.0f;
+    min_p = __fadd_rn(param(a.min_p, a.min_p_all, row), 0.0f);
+    u = a.u != nullptr ? __fadd_rn(a.u[row], 0.0f) : 0.0f;
     greedy = __frcp_rn(T) > 3.402823466e38f;
     r = greedy ? 1.0f : __fdiv_rn(1.0f, T);
     if (greedy) top_k = 1;

@@ -1,5 +1,5 @@
 """GPU tests of sample_tokens at the ends of its range: uniforms of 0 and 1 on rows of
-every length and number of threads, and borders that only exact sums place.
+every length and number of threads, borders that only exact sums place, parameters of -0.
 
 A weight below half a unit, 2^-45 (rows of up to 2^18 entries), counts as none: at u = 0
 the first kept entry that counts is drawn, at u = 1 the last.  Weights are off by up to
@@ -135,3 +135,40 @@ def test_many_rows(specv, R, V, dtype, out):
         alone = specv.sample_tokens(z, u, **kw)
         assert all(torch.equal(x, y) for x, y in zip(found, alone)), f
         assert torch.equal(specv.filter_logits(z, dtype=DT[out], **kw), filtered), f
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("R,V", [(6, 1), (12, 70), (12, 1000), (700, 5003), (12, 20011), (6, 128256)],
+                         ids=str)
+def test_negative_zeros_are_zeros(specv, R, V, dtype):
+    """A parameter or a uniform of -0 is one of 0, as a number and in a tensor."""
+    z = _rows(R, V, V, dtype) if V > 1 else torch.randn((R, 1), device=DEV).to(DT[dtype])
+    u = torch.rand((R,), generator=torch.Generator(device=DEV).manual_seed(V), device=DEV)
+    u[::3] = 0.0
+    each = lambda x: torch.full((R,), x, device=DEV)
+    some = lambda x, y: torch.where(torch.arange(R, device=DEV) % 2 == 0, x, y)
+    cases = [dict(temperature=x) for x in (0.0, each(0.0), some(0.0, 0.7))]
+    cases += [dict(top_p=x) for x in (0.0, each(0.0), some(0.0, 0.9))]
+    cases += [dict(top_p=0.0, top_k=k) for k in (20, 3000)]
+    cases += [dict(temperature=0.0, top_k=50, top_p=0.0, min_p=0.0), dict(min_p=some(0.0, 0.1)), dict()]
+
+    def negated(x):
+        if isinstance(x, torch.Tensor):
+            return torch.where(x == 0, -0.0, x)
+        return -0.0 if isinstance(x, float) and x == 0 else x
+
+    for kw in cases:
+        neg = {k: negated(x) for k, x in kw.items()}
+        for v in neg.values():  # (there is something to test)
+            if isinstance(v, torch.Tensor):
+                assert bool((torch.signbit(v) & (v == 0)).any())
+        out, want = torch.full_like(z, 7.0), torch.full_like(z, 7.0)
+        a = specv.sample_tokens(z, u, out_filtered=want, **kw)
+        b = specv.sample_tokens(z, negated(u), out_filtered=out, **neg)
+        torch.cuda.synchronize()
+        assert bool((a.tokens >= 0).all())
+        assert all(torch.equal(x, y) for x, y in zip(a, b)), kw
+        assert torch.equal(out, want) and torch.equal(specv.filter_logits(z, **neg), want), kw
+        if V > 1 and not isinstance(kw.get("temperature", 1), torch.Tensor) and kw.get("temperature") == 0.0:
+            first = torch.where(z == z.amax(-1, keepdim=True), torch.arange(V, device=DEV), V).amin(-1)
+            assert torch.equal(b.tokens.long(), first)
