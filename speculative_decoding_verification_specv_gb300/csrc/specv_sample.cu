@@ -423,7 +423,8 @@ __device__ __forceinline__ void find_bin(SampleShared<NT> &sh, uint64_t base, ui
   for (int w = 0; w < warp; ++w) at += sh.part2[w];
   if (at < target && at + own >= target) {  // one thread at most
     int b = tid * kEach;
-    while (at + value(b) < target) at += value(b++);
+    // (not past the thread's own bins, whatever the sums are)
+    while ((b + 1) % kEach != 0 && at + value(b) < target) at += value(b++);
     sh.found = b;
     sh.before = at;
   }
@@ -944,7 +945,9 @@ __device__ __noinline__ bool cut_sampled(float limit) {
       for (int e = 0; e < VW; ++e) {
         const float z = Elem<T>::get(v[u], e), d = __fsub_rn(m, z);
         if (!(z > -INFINITY) || (cut && !p.in_order(z, at + e))) continue;
-        if (d < far)
+        // (above m only where a caller writes the row meanwhile: it may come out wrong, but
+        // nothing is counted outside the histogram)
+        if (d >= 0.0f && d < far)
           atomicAdd(&sh.count[linear_bin(m, z)], 1u);
         else if (by_mass)
           tail += ex2(__fmul_rn(-d, rl2));
