@@ -540,7 +540,7 @@ __device__ __forceinline__ void first_pass(SampleShared<NT> &sh, const RowVector
       for (int u = 0; u < kUnroll; ++u) {
         const int k = base + u * 32 + lane;
         v[u] = make_uint4(none, none, none, none);
-        if (k < hi) v[u] = load_vec<T>(row, k);
+        if (k >= row.full_lo && k < plain_hi) v[u] = load16(row.base + (int64_t)k * 16);
       }
     }
   };
@@ -549,6 +549,28 @@ __device__ __forceinline__ void first_pass(SampleShared<NT> &sh, const RowVector
   s = 0.0f;
   const float rl2 = __fmul_rn(r, kLog2e);
   const uint64_t scale = pack2(rl2, rl2);
+  // The reference moves so that the exponents of entries up to `top` stay small.
+  auto move_to = [&](float top, uint64_t &part) {
+    if (__fmul_rn(__fsub_rn(top, ref), r) > 8.0f) {
+      const float f = ex2(fmaxf(__fmul_rn(__fsub_rn(ref, top), rl2), kFarBelow));
+      part = mul2(part, pack2(f, f));
+      s = __fmul_rn(s, f);
+      ref = top;
+    }
+  };
+  auto add_vector = [&](const uint4 &v, uint64_t neg, uint64_t &part) {
+#pragma unroll
+    for (int i = 0; i < Elem<T>::kPerVec / 2; ++i) {
+      float x0, x1;
+      unpack2(mul2(add2(pair_of<T>(v, i), neg), scale), x0, x1);
+      part = add2(part, pack2(ex2(x0), ex2(x1)));
+    }
+  };
+  auto add_part = [&](uint64_t part) {
+    float a, b;
+    unpack2(part, a, b);
+    s = __fadd_rn(s, __fadd_rn(a, b));
+  };
   uint4 cur[kUnroll], next[kUnroll];
   load_batch(lo, cur);
   int base = lo;
@@ -560,31 +582,35 @@ __device__ __forceinline__ void first_pass(SampleShared<NT> &sh, const RowVector
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) top = max_nan(top, vector_max_nan<T>(cur[u]));
       if (SUMS) {
-        if (__fmul_rn(__fsub_rn(top, ref), r) > 8.0f) {
-          const float f = ex2(fmaxf(__fmul_rn(__fsub_rn(ref, top), rl2), kFarBelow));
-          part = mul2(part, pack2(f, f));
-          s = __fmul_rn(s, f);
-          ref = top;
-        }
+        move_to(top, part);
         const uint64_t neg = pack2(-ref, -ref);
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-          for (int i = 0; i < Elem<T>::kPerVec / 2; ++i) {
-            float x0, x1;
-            unpack2(mul2(add2(pair_of<T>(cur[u], i), neg), scale), x0, x1);
-            part = add2(part, pack2(ex2(x0), ex2(x1)));
-          }
+        for (int u = 0; u < kUnroll; ++u) add_vector(cur[u], neg, part);
       }
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) cur[u] = next[u];
     }
     sh.strip[g * NT + tid] = top;
     m = max_nan(m, top);
+    if (SUMS) add_part(part);
+  }
+  // The row's edge vectors, by the lanes that they are dealt to: after the others, when no
+  // loads are in flight that a call would have to save.
+#pragma unroll 1
+  for (int j = 0; j < 2; ++j) {
+    const int k = j == 0 ? 0 : row.full_hi;
+    const bool edge = j == 0 ? row.full_lo > 0 : k < row.count && k >= row.full_lo;
+    if (!edge || k < lo || k >= hi || ((k - lo) & 31) != lane) continue;
+    const uint4 v = load_vec<T>(row, k);
+    const float top = vector_max_nan<T>(v);
+    float &strip = sh.strip[(k - lo) / (kBatch * deal.seg_batches) * NT + tid];
+    strip = max_nan(strip, top);
+    m = max_nan(m, top);
     if (SUMS) {
-      float a, b;
-      unpack2(part, a, b);
-      s = __fadd_rn(s, __fadd_rn(a, b));
+      uint64_t part = 0;
+      move_to(top, part);
+      add_vector(v, pack2(-ref, -ref), part);
+      add_part(part);
     }
   }
 }
@@ -1362,11 +1388,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(
     __syncthreads();
 #pragma unroll 8
     for (int w = 0; w < NT / 32; ++w) about = __fadd_rn(about, sh.fsum[w]);
-    // In units of 2^-24 of the sum.  Additions: a strip's terms, the strips, the merges.
+    // In units of 2^-24 of the sum.  Additions: a strip's terms, the strips, the edges, the merges.
     // Weights, here and by their definition: four roundings each in proportion to the
     // exponent, whose weighted mean is at most ln V, to the 16 that the reference may be off,
     // and the exponentials.
-    const int terms = deal.seg_batches * kUnroll * Elem<T>::kPerVec / 2 + deal.segs + NT / 32 + 8;
+    const int terms = deal.seg_batches * kUnroll * Elem<T>::kPerVec / 2 + deal.segs + NT / 32 + 10;
     off_by = __fmul_rn(about, (float)(terms + 6 * (32 - __clz(a.V)) + 80) * 5.9604645e-8f);
   }
 
