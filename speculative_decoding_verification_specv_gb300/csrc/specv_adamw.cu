@@ -183,7 +183,10 @@ __device__ __forceinline__ void decode(uint32_t four, float scale, float *x) {
 
 // What maps a block x whose largest magnitude is `top` to e4m3 times 2^-120: (the scale, the
 // factor).  Below 2^-100 the block is stored as zeros; a top that is not finite makes the
-// scale NaN.  From 2^14 on the factor would leave fp32's normal numbers: x is made smaller.
+// scale NaN.  From 2^14 on the factor would leave fp32's normal numbers: x is made smaller,
+// a ROOT that is not 0 not below 2^-100, so that it is still known from 0 (either way its code
+// is the smallest one).
+template <bool ROOT>
 __device__ __forceinline__ float2 block_scale(float top, float (&x)[8]) {
   constexpr float kDown = 7.52316384526264e-37f;  // 2^-120
   if (top < kTiny) return make_float2(0.0f, 0.0f);
@@ -191,7 +194,11 @@ __device__ __forceinline__ float2 block_scale(float top, float (&x)[8]) {
   const float scale = __fmul_rn(top, 1.0f / 448.0f);
   if (top >= 16384.0f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(x[i], 5.421010862427522e-20f);  // 2^-64
+    for (int i = 0; i < 8; ++i) {
+      const float least = ROOT ? fminf(x[i], kTiny) : 0.0f;
+      x[i] = __fmul_rn(x[i], 5.421010862427522e-20f);  // 2^-64
+      if (ROOT) x[i] = fmaxf(x[i], least);
+    }
     top = __fmul_rn(top, 5.421010862427522e-20f);
   }
   return make_float2(scale, __fmul_rn(__fmul_rn(448.0f, __frcp_rn(top)), kDown));
@@ -313,7 +320,7 @@ __device__ __forceinline__ void step_block(const Tensor &x, const Factors &f, in
   }
   top_m = warp_top(top_m);
   top_v = warp_top(top_v);
-  const float2 fm = block_scale(top_m, m), fv = block_scale(top_v, v);
+  const float2 fm = block_scale<false>(top_m, m), fv = block_scale<true>(top_v, v);
   // The hash of an entry is that of its index added to the tensor's key; its first product
   // is taken once for the block.  (A block begins at a multiple of 256: no carry into the
   // index's upper half.)
@@ -326,7 +333,7 @@ __device__ __forceinline__ void step_block(const Tensor &x, const Factors &f, in
     const uint32_t upper = ((h >> 8) & 0xffff00u) | 0x80u;
     const uint32_t lower = ((h << 8) ^ upper) & 0xffff80u;
     em[i] = code_of(__fmul_rn(fabsf(m[i]), fm.y), upper) | (__float_as_uint(m[i]) & 0x80000000u);
-    // (a root that is not 0 is above 2^-64: at least the smallest code)
+    // (a root that is not 0 is above 2^-101: at least the smallest code)
     ev[i] = max(code_of(__fmul_rn(v[i], fv.y), lower), min(__float_as_uint(v[i]), 1u << 24));
   }
   store_codes(x.m, at, left, vec, make_uint2(upper_bytes(em), upper_bytes(em + 4)));

@@ -1,0 +1,47 @@
+"""GPU tests of adamw_step at the ends of its ranges: blocks of 8-bit roots that lie far
+apart."""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module")
+def specv():
+    if not torch.cuda.is_available():
+        pytest.fail("a CUDA device is required for the gpu tests")
+    import speculative_decoding_verification_specv_gb300 as m
+    m.load(build_if_missing=True)
+    return m
+
+
+@pytest.mark.parametrize("n", [1024, 1021])
+@pytest.mark.parametrize("large", [1e3, 5e5, 1e6, 1e9, 1e15])
+def test_small_roots_beside_large_ones(specv, large, n):
+    """A root that is not 0 is stored as the smallest positive value at least: its weight would
+    move by m / eps otherwise.  From zero states the root is sqrt(1 - beta2) |g|; gradients from
+    2^-57 on have squares, times 1 - beta2, of at least 2^-124, in fp32's normal numbers, so
+    their roots are not 0.  The second block has no large one; the third only zeros."""
+    p = torch.zeros(n, device=DEV)
+    g = torch.zeros(n, device=DEV)
+    sizes = 2.0 ** -torch.arange(0, 57.5, 0.5, device=DEV)
+    g[:256:2] = sizes.repeat(3)[:128]
+    g[100], g[32] = large, -large
+    g[256:512:2] = sizes.repeat(3)[:128]
+    g[700:] = 0
+    st = specv.adamw_state([p], 8)
+    for t in (1, 2, 3):
+        specv.adamw_step([p], [g], st, t, 1e-3, seed=t)
+        torch.cuda.synchronize()
+        codes = st.exp_avg_sq[0].view(torch.uint8)
+        assert bool((codes[g != 0] >= 1).all()), int((codes[g != 0] == 0).sum())
+        assert bool((codes[g == 0] == 0).all())
+        # smaller than the smallest value by far: exactly that one
+        far = (g != 0) & (torch.arange(n, device=DEV) < 256) & (g.abs() < large * 2.0 ** -30)
+        assert bool((codes[far] == 1).all()) and (int(far.sum()) > 0 or large < 1e4)
+        s = st.scales[0][:, 1].double()
+        want = large * math.sqrt(1 - 0.999 ** t) / 448
+        assert abs(float(s[0]) - want) <= want * 2.0 ** -4  # (the stored root is rounded each step)
