@@ -85,8 +85,8 @@ def adamw_step(params, grads, state, step, lr, betas=(0.9, 0.999), eps: float = 
     """One AdamW step over many tensors, in place.
 
     params and grads: float32 and bfloat16 CUDA tensors of one device, contiguous, of any
-    shapes (empty ones too), none twice; a gradient has its weight's size and either
-    type.  state: an AdamWState (adamw_state makes the first), or its four fields.
+    shapes (empty ones too), none twice; a gradient has its weight's shape (or the same
+    entries in one dimension, as the state may) and either type.  state: an AdamWState (adamw_state makes the first), or its four fields.
     step: the step's number, from 1 on; lr: the learning rate.  Either may be a CUDA
     tensor of one element (int32, float32), which a captured graph reads anew at each
     replay.  eps: 0, or a normal float32 number.  weight_decay: a number, or one for each
@@ -150,6 +150,17 @@ def adamw_step(params, grads, state, step, lr, betas=(0.9, 0.999), eps: float = 
         pass
     if types is None or any(len(t) != lengths[name] for name, t, _, _ in lists):
         _why(lists, lengths, dev, counts)
+    # Of two matrices of one size, one may be the other's transpose: shapes have to agree.
+    # (Flat ones may stand for any shape.)
+    deep = [i for i, d in enumerate(map(_Tensor.dim, params)) if d > 1]
+    if deep:
+        for name, tensors, of in (("grads", grads, deep), ("exp_avg", exp_avg, deep),
+                                  ("exp_avg_sq", exp_avg_sq, deep),
+                                  ("masters", masters, [i for i in some if params[i].dim() > 1])):
+            for i in of:
+                if tensors[i].shape != params[i].shape and tensors[i].dim() > 1:
+                    raise ValueError(f"{name} must match the weights in shape: "
+                                     f"{tuple(params[i].shape)}, got {tuple(tensors[i].shape)}")
     at = list(map(_Tensor.data_ptr, every))
     # (gradients are only read: one may serve several weights)
     live = [p for p, c in zip(at[:n] + at[2 * n:], counts + sizes[2 * n:]) if c]
