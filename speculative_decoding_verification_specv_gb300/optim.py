@@ -26,6 +26,7 @@ _pack = struct.Struct("qqddddPPPfIQ").pack
 _WORDS = 10  # of specv_adamw_tensor
 _EITHER = (torch.float32, torch.bfloat16)
 _dtype_of, _get_device = attrgetter("dtype"), _Tensor.get_device
+_written = torch.autograd.graph.increment_version
 
 
 class AdamWState(NamedTuple):
@@ -97,14 +98,19 @@ def adamw_step(params, grads, state, step, lr, betas=(0.9, 0.999), eps: float = 
     ``clip_grads(grads, math.inf)``).  A norm that is not finite leaves weights and state
     as they are.
 
+    As after any step in place, autograd refuses to go back through a graph that saved the
+    weights before it.  (A replayed CUDA graph writes them unseen.)
+
     8-bit states are rounded at random, reproducibly: by ``seed``, the step, the tensor's
     place in the list and the entry's place in the tensor.
     """
     params, grads = list(params), list(grads)
     exp_avg, exp_avg_sq, scales, masters = state
     n = len(params)
-    if not all(isinstance(p, _Tensor) for p in params):
-        raise TypeError("params must hold tensors")
+    try:
+        counts = list(map(_Tensor.numel, params))
+    except TypeError:
+        raise TypeError("params must hold tensors") from None
     if n:
         dev = params[0].device
         if dev.type != "cuda":
@@ -115,7 +121,6 @@ def adamw_step(params, grads, state, step, lr, betas=(0.9, 0.999), eps: float = 
         dev = torch.device("cuda", torch.cuda.current_device())
     bits = 32 if scales is None else 8
     # A call is short on the GPU: all tensors are looked at together, in a few passes.
-    counts = list(map(_Tensor.numel, params))
     exp_avg, exp_avg_sq = list(exp_avg), list(exp_avg_sq)
     kind = (_f32,) if bits == 32 else (_f8,)
     lists = [("params", params, counts, _EITHER), ("grads", grads, counts, _EITHER),
@@ -163,9 +168,11 @@ def adamw_step(params, grads, state, step, lr, betas=(0.9, 0.999), eps: float = 
                                      f"{tuple(params[i].shape)}, got {tuple(tensors[i].shape)}")
     at = list(map(_Tensor.data_ptr, every))
     # (gradients are only read: one may serve several weights)
-    live = [p for p, c in zip(at[:n] + at[2 * n:], counts + sizes[2 * n:]) if c]
-    if len(set(live)) != len(live):
-        raise ValueError("a weight, a state or a master is listed twice")
+    live = at[:n] + at[2 * n:]
+    if len(set(live)) != len(live):  # (empty tensors may share an address)
+        live = [p for p, c in zip(live, counts + sizes[2 * n:]) if c]
+        if len(set(live)) != len(live):
+            raise ValueError("a weight, a state or a master is listed twice")
     table = array("q", bytes(8 * _WORDS * n))
     for k in range(5 if bits == 8 else 4):
         table[k::_WORDS] = array("q", at[k * n:(k + 1) * n])
@@ -220,3 +227,5 @@ def adamw_step(params, grads, state, step, lr, betas=(0.9, 0.999), eps: float = 
                                             _stream(dev))
     if st:
         _check(st, "specv_adamw_step")
+    # a graph that saved a weight sees that it was written
+    _written(params if not some else params + [masters[i] for i in some])

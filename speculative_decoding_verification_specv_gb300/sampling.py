@@ -16,6 +16,7 @@ from . import BF16, F32, _check, _dtype_code
 from .scoring import _elsewhere, _entry, _fit, _rows, _stream
 
 _Tensor, _empty, _f32, _i32 = torch.Tensor, torch.empty, torch.float32, torch.int32
+_written = torch.autograd.graph.increment_version  # a graph that saved the tensor sees it
 # specv_sampling: four pointers and, for those that are NULL, the values for all rows
 _pack = struct.Struct("PPPPfiff").pack
 
@@ -115,6 +116,8 @@ def sample_tokens(logits, u, temperature=None, top_k=None, top_p=None, min_p=Non
         None if out_filtered is None else out_filtered.data_ptr(), out_code, _stream(dev))
     if st:
         _check(st, "specv_sample_tokens")
+    if out_filtered is not None:
+        _written(out_filtered)
     return SampledTokens(tokens, logprobs, lse)
 
 
@@ -150,10 +153,13 @@ def filter_logits(logits, temperature=None, top_k=None, top_p=None, min_p=None, 
     if there is not None:
         with there:
             return filter_logits(logits, temperature, top_k, top_p, min_p, out, dtype)
-    if out is None:
+    given = out is not None
+    if not given:
         out = _empty(logits.shape, dtype=dtype, device=dev)
     st = _entry("specv_filter_logits")(logits.data_ptr(), params, B, N, V, sb, sn, code,
                                        out.data_ptr(), out_code, _stream(dev))
     if st:
         _check(st, "specv_filter_logits")
+    if given:
+        _written(out)
     return out

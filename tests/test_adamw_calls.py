@@ -1,4 +1,4 @@
-"""adamw_step's host side without a GPU: tensors in host memory that call themselves a GPU's,
+"""adamw_step's host side without a GPU (and what sampling shares with it): tensors in host memory that call themselves a GPU's,
 and the library's entry replaced by one that notes the call."""
 import math
 
@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import speculative_decoding_verification_specv_gb300 as specv
-from speculative_decoding_verification_specv_gb300 import optim
+from speculative_decoding_verification_specv_gb300 import optim, sampling
 
 
 class OnGpu(torch.Tensor):
@@ -31,8 +31,11 @@ def calls(monkeypatch):
 
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 7, raising=False)
-    monkeypatch.setattr(optim, "_entry", entry)
+    for module in (optim, sampling):
+        monkeypatch.setattr(module, "_entry", entry)
     monkeypatch.setattr(optim, "_get_device", lambda t: t.device.index)
+    monkeypatch.setattr(sampling, "_empty",
+                        lambda shape, dtype, device: torch.zeros(shape, dtype=dtype).as_subclass(OnGpu))
     return made
 
 
@@ -63,3 +66,27 @@ def test_shapes_have_to_agree(calls):
     specv.adamw_step(other(p, 1, _t(12)), g, st, 1, 0.1)
     specv.adamw_step(half, g, st._replace(masters=[None, _t(12), None]), 1, 0.1)
     assert len(calls) == 4
+
+
+def test_what_is_written_counts_as_written(calls):
+    """In place means in place for autograd too: version counters move."""
+    p = [_t(5), _t(3, 4, dtype=torch.bfloat16)]
+    masters = [None, _t(3, 4)]
+    g = [_t(5), _t(3, 4)]
+    before = [x._version for x in (*p, masters[1], *g)]
+    specv.adamw_step(p, g, _state(p, masters), 1, 0.1)
+    assert [x._version for x in (*p, masters[1])] == [v + 1 for v in before[:3]]
+    assert [x._version for x in g] == before[3:]  # read only
+    with torch.inference_mode():
+        q = [_t(5)]
+    specv.adamw_step(q, g[:1], _state(q), 1, 0.1)
+    z, u, out = _t(2, 3, 8), _t(2, 3), _t(2, 3, 8)
+    before = z._version, out._version
+    specv.filter_logits(z, 0.7, out=out)
+    specv.sample_tokens(z, u, out_filtered=out)
+    assert (z._version, out._version) == (before[0], before[1] + 2)
+    specv.filter_logits(z, 0.7, out=z)
+    assert z._version == before[0] + 1
+    specv.filter_logits(z, 0.7)
+    specv.sample_tokens(z, u)
+    assert z._version == before[0] + 1

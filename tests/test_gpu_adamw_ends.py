@@ -1,5 +1,5 @@
 """GPU tests of adamw_step at the ends of its ranges: blocks of 8-bit roots that lie far
-apart."""
+apart, and graphs that saved a weight."""
 import math
 
 import pytest
@@ -45,3 +45,26 @@ def test_small_roots_beside_large_ones(specv, large, n):
         s = st.scales[0][:, 1].double()
         want = large * math.sqrt(1 - 0.999 ** t) / 448
         assert abs(float(s[0]) - want) <= want * 2.0 ** -4  # (the stored root is rounded each step)
+
+
+def test_a_graph_that_saved_a_weight_refuses_to_go_back(specv):
+    """As with any step in place: its gradients would be those of other weights."""
+    x = torch.ones((4, 3), device=DEV, requires_grad=True)
+    w = torch.nn.Parameter(torch.ones((5, 3), device=DEV))
+    y = (x @ w.T).square().sum()
+    y.backward(retain_graph=True)
+    st = specv.adamw_state([w])
+    specv.adamw_step([w], [w.grad], st, 1, 0.1)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    z = torch.randn((2, 50), device=DEV, requires_grad=True)
+    rows = z * 1.0
+    loss = rows.square().sum()
+    specv.filter_logits(rows.detach(), top_k=3, out=rows.detach())
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    # a step after the backward pass is what a training loop does
+    for t in (2, 3):
+        w.grad = None
+        (x @ w.T).square().sum().backward()
+        specv.adamw_step([w], [w.grad], st, t, 0.1)
