@@ -25,6 +25,7 @@ BLOCK = 256  # entries of an 8-bit state that share a scale
 _pack = struct.Struct("qqddddPPPfIQ").pack
 _WORDS = 10  # of specv_adamw_tensor
 _EITHER = (torch.float32, torch.bfloat16)
+_MOST = torch.finfo(torch.float32).max
 _dtype_of, _get_device = attrgetter("dtype"), _Tensor.get_device
 _written = torch.autograd.graph.increment_version
 
@@ -211,11 +212,13 @@ def adamw_step(params, grads, state, step, lr, betas=(0.9, 0.999), eps: float = 
     max_norm = float(max_norm)
     if not max_norm >= 0.0:
         raise ValueError("max_norm must be >= 0")
+    if max_norm > _MOST:  # no norm in float32 exceeds it
+        max_norm = math.inf
     if norm is not None:
         norm_at = _scalar(norm, "norm", _f32, dev)
     elif max_norm != math.inf:
         raise ValueError("max_norm needs the gradients' norm")
-    config = _pack(bits, step, lr, b1, b2, eps, step_at, lr_at, norm_at, min(max_norm, 3.4e38), 0,
+    config = _pack(bits, step, lr, b1, b2, eps, step_at, lr_at, norm_at, max_norm, 0,
                    seed & 0xFFFFFFFFFFFFFFFF)
     there = _elsewhere(stream, dev)
     if there is None:

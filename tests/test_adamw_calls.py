@@ -1,6 +1,7 @@
 """adamw_step's host side without a GPU (and what sampling shares with it): tensors in host memory that call themselves a GPU's,
 and the library's entry replaced by one that notes the call."""
 import math
+import struct
 
 import pytest
 import torch
@@ -90,3 +91,12 @@ def test_what_is_written_counts_as_written(calls):
     specv.filter_logits(z, 0.7)
     specv.sample_tokens(z, u)
     assert z._version == before[0] + 1
+
+
+@pytest.mark.parametrize("max_norm,there", [(1.0, 1.0), (0.0, 0.0), (3.4e38, 3.4e38), (1e39, math.inf),
+                                            (math.inf, math.inf)])
+def test_the_largest_norm_as_it_is_given(calls, max_norm, there):
+    p, norm = [_t(5)], _t(1)
+    specv.adamw_step(p, [_t(5)], _state(p), 1, 0.1, norm=norm, max_norm=max_norm)
+    config = calls.pop()[1][2]
+    assert struct.unpack("qqddddPPPfIQ", config)[9] == torch.tensor(there).item()

@@ -1,5 +1,5 @@
 """GPU tests of adamw_step at the ends of its ranges: blocks of 8-bit roots that lie far
-apart, and graphs that saved a weight."""
+apart, graphs that saved a weight, norms near fp32's largest."""
 import math
 
 import pytest
@@ -68,3 +68,19 @@ def test_a_graph_that_saved_a_weight_refuses_to_go_back(specv):
         w.grad = None
         (x @ w.T).square().sum().backward()
         specv.adamw_step([w], [w.grad], st, t, 0.1)
+
+
+@pytest.mark.parametrize("max_norm", [math.inf, 1e39, torch.finfo(torch.float32).max])
+def test_a_limit_that_no_norm_exceeds(specv, max_norm):
+    """min(1, max_norm / (norm + 1e-6)) is 1 for any finite norm."""
+    n = 3000
+    for norm in (torch.finfo(torch.float32).max, 3.39e38, 1.0, 0.0):
+        both = []
+        for kw in (dict(), dict(norm=torch.tensor(norm, device=DEV), max_norm=max_norm)):
+            p = [torch.linspace(-1, 1, n, device=DEV)]
+            g = [torch.linspace(-3e-3, 2e-3, n, device=DEV)]
+            st = specv.adamw_state(p)
+            specv.adamw_step(p, g, st, 1, 0.1, **kw)
+            both.append((p[0], st.exp_avg[0], st.exp_avg_sq[0]))
+        for x, y in zip(*both):
+            assert torch.equal(x, y), norm
