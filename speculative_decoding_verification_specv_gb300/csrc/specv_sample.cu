@@ -601,7 +601,8 @@ __device__ __forceinline__ void first_pass(SampleShared<NT> &sh, const RowVector
     const int k = j == 0 ? 0 : row.full_hi;
     const bool edge = j == 0 ? row.full_lo > 0 : k < row.count && k >= row.full_lo;
     if (!edge || k < lo || k >= hi || ((k - lo) & 31) != lane) continue;
-    const uint4 v = load_vec<T>(row, k);
+    const uint4 v = load_part<T>(row.base + (int64_t)k * 16, k == 0 ? row.mis : 0,
+                                 (int)min((int64_t)Elem<T>::kPerVec, row.V - row.index(k, 0)));
     const float top = vector_max_nan<T>(v);
     float &strip = sh.strip[(k - lo) / (kBatch * deal.seg_batches) * NT + tid];
     strip = max_nan(strip, top);
