@@ -715,7 +715,9 @@ typedef struct {
  * largest magnitude / 448 and rounds every value to one of the two nearest e4m3 values
  * at random, up with the probability of its distance from the lower (16 bits, a hash of
  * seed, t, the tensor's place in the list and the entry's index: the same call gives the
- * same state).  A root that is not 0 is stored as the smallest positive value at least.
+ * same state).  The hash is one sequence of 2^32 draws, which each seed, step and place
+ * begins at a point of its own: long tensors, or many steps, meet parts of it again, shifted
+ * against the entries.  A root that is not 0 is stored as the smallest positive value at least.
  * A block of m whose largest magnitude is below 2^-100 is stored as zeros.  A value that is
  * not finite makes its whole block NaN.  All zero (scales too) is the state before the
  * first step, in 8 bits as in 32.

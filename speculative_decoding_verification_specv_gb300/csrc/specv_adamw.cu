@@ -17,8 +17,10 @@
 // entry maps to 448, so the scale follows the state itself.  Values are rounded up or
 // down at random with the probability of the distance: an average that moves by one part
 // in a thousand per step would never leave a value rounded to nearest 4 bits.  The bits
-// are a hash of (seed, step, tensor, entry), 16 for each value.  A root that is not 0 is
-// never stored as 0: its weight would move by m / eps.
+// are a hash of (seed, step, tensor, entry), 16 for each value: the entry's index added to a
+// key of 32 bits, so tensors and steps take stretches of one sequence of 2^32 (stretches that
+// overlap are shifted against the entries, and a value's rounding stays unbiased).  A root that
+// is not 0 is never stored as 0: its weight would move by m / eps.
 //
 // 32-bit states are bound by HBM: 434 M weights, most bf16 with masters (12.1 GB), 1702 us, 7.1 TB/s,
 // above the copy rate since more is read than written.  8-bit states by instructions, 55 for
