@@ -1,5 +1,5 @@
 """GPU tests of sample_tokens at the ends of its range: uniforms of 0 and 1 on rows of
-every length and number of threads, borders that only exact sums place, parameters of -0.
+every length and number of threads, borders that only exact sums place, parameters of -0, the longest row.
 
 A weight below half a unit, 2^-45 (rows of up to 2^18 entries), counts as none: at u = 0
 the first kept entry that counts is drawn, at u = 1 the last.  Weights are off by up to
@@ -172,3 +172,35 @@ def test_negative_zeros_are_zeros(specv, R, V, dtype):
         if V > 1 and not isinstance(kw.get("temperature", 1), torch.Tensor) and kw.get("temperature") == 0.0:
             first = torch.where(z == z.amax(-1, keepdim=True), torch.arange(V, device=DEV), V).amin(-1)
             assert torch.equal(b.tokens.long(), first)
+
+
+def test_the_longest_row(specv):
+    """2^31 - 1 entries, 18, 20 and 19 among entries of -20: those weigh 2^-57, below half a
+    unit (2^-31 here), and count as none in the sums; the three hold 0.09, 0.665 and 0.245 of
+    the whole."""
+    V = (1 << 31) - 1
+    at = [5, (1 << 30) + 1, V - 2]
+    z = torch.full((1, V), -20.0, dtype=torch.bfloat16, device=DEV)
+    z[0, at] = torch.tensor([18.0, 20.0, 19.0], dtype=torch.bfloat16, device=DEV)
+    share = torch.softmax(torch.tensor([18.0, 20.0, 19.0], dtype=torch.float64), 0)
+    out = torch.empty_like(z)
+    for kw, kept in ((dict(), [0, 1, 2]), (dict(top_k=2), [1, 2]), (dict(top_p=0.5), [1]),
+                     (dict(top_p=0.9), [1, 2]), (dict(min_p=0.2), [1, 2]), (dict(temperature=0.0), [1]),
+                     (dict(top_k=100000), [0, 1, 2]), (dict(top_k=100000, top_p=0.9), [1, 2])):
+        p = share[kept] / share[kept].sum()
+        upto = p.cumsum(0)
+        filtered = specv.filter_logits(z, out=out, **kw)
+        some = int((filtered > NEG).sum())
+        if kw == dict():
+            assert some == V
+        elif kw == dict(top_k=100000):  # the three and the first others, in index order
+            assert some == 100000 and bool((filtered[0, : 100000 - 2] > NEG).all())
+        else:
+            assert some == len(kept)
+        for j in kept:
+            assert float(filtered[0, at[j]]) == (0.0 if "temperature" in kw else float(z[0, at[j]]))
+        for u, j in ((0.0, 0), (0.5, int((upto <= 0.5).sum())), (1.0, len(kept) - 1)):
+            found = specv.sample_tokens(z, torch.full((1,), u, device=DEV), **kw)
+            assert int(found.tokens[0]) == at[kept[j]], (kw, u)
+            # (the sum of a row that nothing filters is in fp32, off by some hundred roundings)
+            assert abs(float(found.logprobs[0]) - math.log(p[j])) <= 1e-4, (kw, u)
