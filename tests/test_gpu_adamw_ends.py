@@ -84,3 +84,22 @@ def test_a_limit_that_no_norm_exceeds(specv, max_norm):
             both.append((p[0], st.exp_avg[0], st.exp_avg_sq[0]))
         for x, y in zip(*both):
             assert torch.equal(x, y), norm
+
+
+def test_under_inference_mode(specv):
+    """Tensors made there have no version counters to move."""
+    with torch.inference_mode():
+        p, g = [torch.ones(3000, device=DEV)], [torch.full((3000,), 0.5, device=DEV)]
+        st = specv.adamw_state(p)
+        specv.adamw_step(p, g, st, 1, 0.1)
+        z, u = torch.randn((4, 5000), device=DEV), torch.rand(4, device=DEV)
+        want = specv.filter_logits(z, top_k=9)
+        drawn = specv.sample_tokens(z, u, top_k=9, out_filtered=z)
+        again = specv.filter_logits(z, top_k=9, out=z)
+    w = torch.ones(3000, device=DEV)  # (an ordinary tensor too)
+    with torch.inference_mode():
+        specv.adamw_step([w], g, specv.adamw_state([w]), 1, 0.1)
+    torch.cuda.synchronize()
+    assert bool(((p[0] - 0.9).abs() <= 1e-6).all()) and torch.equal(w, p[0])
+    assert torch.equal(z, want) and again is z
+    assert bool((want.gather(-1, drawn.tokens.long().unsqueeze(-1)) > -math.inf).all())
