@@ -629,8 +629,8 @@ typedef struct {
  *
  * Weights are fp32, the largest 1; the sums that decide (a share, a running sum) are of whole
  * numbers of 2^-44 (V above 2^18: of 2^-62 times the next power of two from V on), each weight
- * rounded to one, so that the result does not depend on the launch.  A weight below half of
- * that counts as none.  (The log probability of a row that nothing filters takes an fp32 sum.)  A -inf logit masks its entry: it is never kept.  A row that masks every
+ * rounded to one, so that the result does not depend on the launch (V above 2^25: but where the
+ * weights below half a unit decide).  A weight below half of that counts as none.  (The log probability of a row that nothing filters takes an fp32 sum.)  A -inf logit masks its entry: it is never kept.  A row that masks every
  * entry gives token -1, log probability 0 and log-normaliser -inf.  A row with a NaN or
  * +inf, a parameter outside its range or a u outside [0, 1] gives token -1 and NaN (its
  * filtered row too).  No scratch, no allocation; asynchronous on `stream`; host argument

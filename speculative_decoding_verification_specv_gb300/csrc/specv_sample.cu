@@ -39,7 +39,7 @@
 // (1.05 GB, 157 us at the copy rate; 313): top-k 50 192 us (368), min-p 0.05 170 (350),
 // nothing 316 to filter; bound by HBM.  Nothing 237 to 289 to sample: the second read of an
 // eighth of the row, and of all of it where u W lies too close to a border to tell.  top-p
-// 0.95: 304 us where every row has some likely entries, 679 where all are flat: bound by
+// 0.95: 300 us where every row has some likely entries, 691 where all are flat: bound by
 // instructions, some forty for each entry of the pass over the whole row; one flat row of
 // bf16 66.  One with top-k 50 and top-p 0.9 17 us, bound by a dozen barriers and loads that
 // wait for one another.
@@ -594,15 +594,15 @@ __device__ __forceinline__ void first_pass(SampleShared<NT> &sh, const RowVector
     m = max_nan(m, top);
     if (SUMS) add_part(part);
   }
-  // The row's edge vectors, by the lanes that they are dealt to: after the others, when no
-  // loads are in flight that a call would have to save.
+  // The row's edge vectors, entry by entry, by the lanes that they are dealt to: after the
+  // others, when no loads are in flight that a call would have to save (amid them, one
+  // request's row 18.7 us against 16.6, 2304 rows under top-k and top-p 398 against 390).
 #pragma unroll 1
   for (int j = 0; j < 2; ++j) {
     const int k = j == 0 ? 0 : row.full_hi;
     const bool edge = j == 0 ? row.full_lo > 0 : k < row.count && k >= row.full_lo;
     if (!edge || k < lo || k >= hi || ((k - lo) & 31) != lane) continue;
-    const uint4 v = load_part<T>(row.base + (int64_t)k * 16, k == 0 ? row.mis : 0,
-                                 (int)min((int64_t)Elem<T>::kPerVec, row.V - row.index(k, 0)));
+    const uint4 v = load_entries<T>(row.row, row.index(k, 0), row.V);
     const float top = vector_max_nan<T>(v);
     float &strip = sh.strip[(k - lo) / (kBatch * deal.seg_batches) * NT + tid];
     strip = max_nan(strip, top);
@@ -924,9 +924,9 @@ __device__ __noinline__ bool narrow_bracket() {
 // sample's own counts, two standard deviations either way; for a mass by what lies beyond a
 // bin, estimated from the sample as well, against the part of the whole that may (the
 // sample's many light entries say that well, its few heavy ones would not say the rest),
-// 2.4 deviations either way, to a part of a bin.  Twice the entries sampled and 2.4 for 1.7
-// deviations: 64 flat rows of 128256 under top-p 0.95 59 us, from 77 (a miss costs a pass, and the
-// slowest row decides); 2048 such rows 696 from 656.
+// 2.4 deviations either way, to a part of a bin.  Half the entries sampled and
+// 1.7 deviations: 64 flat rows of 128256 under top-p 0.95 66 us against 68 in fp32, 82 against 68
+// in bf16 (a miss costs a pass, and the slowest row decides); 2048 such rows 646 against 692.
 // Where a pass does not find the target in the bracket it says where to go on.  Returns
 // whether it was found (else nothing is set).  `limit`: the first top_k entries have m - z
 // below it.

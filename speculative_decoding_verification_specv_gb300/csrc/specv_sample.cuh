@@ -18,38 +18,9 @@ __device__ __forceinline__ uint4 load16(const char *p) {
                : "l"(p));
   return x;
 }
-// Entries [from, to) of the aligned vector at `at`; -inf for the others.  Whole words, and
-// the halves at the ends: few registers, so that what the callers have in flight keeps its
-// own (entry by entry, with four registers more: filtering 2304 rows of 128256 fp32 entries
-// under top-k and top-p 398 us, 390 this way).
-template <typename T>
-__device__ __noinline__ uint4 load_part(const char *at, int from, int to) {
-  constexpr uint32_t none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
-  uint32_t x[4] = {none, none, none, none};
-  constexpr int kEach = 4 / (int)sizeof(T);
-#pragma unroll
-  for (int w = 0; w < 4; ++w)
-    if (w * kEach >= from && (w + 1) * kEach <= to)
-      asm volatile("ld.global.u32 %0, [%1];" : "=r"(x[w]) : "l"(at + 4 * w));
-  if constexpr (kEach == 2) {
-    uint16_t first = 0xff80, last = 0xff80;
-    if (from & 1) asm volatile("ld.global.u16 %0, [%1];" : "=h"(first) : "l"(at + 2 * from));
-    if (to & 1) asm volatile("ld.global.u16 %0, [%1];" : "=h"(last) : "l"(at + 2 * to - 2));
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      if (from == 2 * w + 1) x[w] = (uint32_t)first << 16 | 0xff80u;
-      if (to == 2 * w + 1) x[w] = 0xff800000u | last;
-    }
-  }
-  return make_uint4(x[0], x[1], x[2], x[3]);
-}
 template <typename T>
 __device__ __forceinline__ uint4 load_vec(const RowVectors<T> &row, int k) {
-  if (k < row.lo || k >= row.hi) {
-    const int64_t first = row.index(k, 0);
-    return load_part<T>(row.base + (int64_t)k * 16, first < 0 ? (int)-first : 0,
-                        (int)min((int64_t)Elem<T>::kPerVec, row.V - first));
-  }
+  if (k < row.lo || k >= row.hi) return load_entries<T>(row.row, row.index(k, 0), row.V);
   uint4 v = load16(row.base + (int64_t)k * 16);
   if (k < row.full_lo || k >= row.full_hi) mask_outside<T>(v, row.index(k, 0), row.V);
   return v;
