@@ -629,13 +629,14 @@ typedef struct {
  *
  * Weights are fp32, the largest 1; the sums that decide (a share, a running sum) are of whole
  * numbers of 2^-44 (V above 2^18: of 2^-62 times the next power of two from V on), each weight
- * rounded to one, so that the result does not depend on the launch (V above 2^25: but where the
- * weights below half a unit decide).  A weight below half of that counts as none.  (The log probability of a row that nothing filters takes an fp32 sum.)  A -inf logit masks its entry: it is never kept.  A row that masks every
- * entry gives token -1, log probability 0 and log-normaliser -inf.  A row with a NaN or
- * +inf, a parameter outside its range or a u outside [0, 1] gives token -1 and NaN (its
- * filtered row too).  No scratch, no allocation; asynchronous on `stream`; host argument
- * errors (a value for all rows outside its range among them) return
- * SPECV_ERR_INVALID_ARG and launch nothing.
+ * rounded to one, so that the result does not depend on the launch (V above 2^25: but where
+ * the weights below half a unit decide).  A weight below half of that counts as none.  (The
+ * log probability of a row that nothing filters takes an fp32 sum.)  A -inf logit masks its
+ * entry: it is never kept.  A row that masks every entry gives token -1, log probability 0
+ * and log-normaliser -inf.  A row with a NaN or +inf, a parameter outside its range or a u
+ * outside [0, 1] gives token -1 and NaN (its filtered row too).  No scratch, no allocation;
+ * asynchronous on `stream`; host argument errors (a value for all rows outside its range
+ * among them) return SPECV_ERR_INVALID_ARG and launch nothing.
  */
 specv_status specv_sample_tokens(const void *logits, const float *u, const specv_sampling *params,
                                  int64_t B, int32_t N, int32_t V, int64_t stride_b,
@@ -703,8 +704,7 @@ typedef struct {
  *   p' = p (1 - lr weight_decay)
  *        - lr / (1 - beta1^t) m' / (sqrt(v') / sqrt(1 - beta2^t) + eps)
  *
- * in fp32 (the root, the quotient and the step's products to a few ulp; a v' below 2^-126
- * has the root 0); p' is rounded once to the weight's type, and kept in fp32 in the master where
+ * in fp32 (the root, the quotient and the step's products to a few ulp); p' is rounded once to the weight's type, and kept in fp32 in the master where
  * there is one (the weight itself is then only written).  With a norm the step clips
  * while it reads, and specv_clip_grads need only measure (max_norm = inf).  A norm that
  * is not finite, or a step on the device below 1, leaves everything as it is.

@@ -1,5 +1,6 @@
 """GPU tests of adamw_step at the ends of its ranges: blocks of 8-bit roots that lie far
-apart, graphs that saved a weight, norms near fp32's largest."""
+apart, graphs that saved a weight, norms near fp32's largest,
+squares below its normal numbers."""
 import math
 
 import pytest
@@ -103,3 +104,21 @@ def test_under_inference_mode(specv):
     assert bool(((p[0] - 0.9).abs() <= 1e-6).all()) and torch.equal(w, p[0])
     assert torch.equal(z, want) and again is z
     assert bool((want.gather(-1, drawn.tokens.long().unsqueeze(-1)) > -math.inf).all())
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_squares_below_the_normal_numbers(specv, bits):
+    """With eps = 0 the first step is the rate against the gradient's sign whatever its size.  v
+    is off by half of fp32's smallest spacing, 2^-150, besides its roundings, its root by half
+    of that in proportion: the weight (0 before) by that much of the rate and some 2^-20."""
+    for k in range(40, 67):
+        g = torch.full((600,), 2.0 ** -k, device=DEV)
+        g[::3] *= -1.0
+        p = torch.zeros(600, device=DEV)
+        st = specv.adamw_state([p], bits)
+        specv.adamw_step([p], [g], st, 1, 0.25, eps=0.0)
+        v = 1e-3 * 2.0 ** (-2 * k)
+        tol = 0.25 * (0.5 * 2.0 ** -150 / v * (1 + 2.0 ** -7) + 2.0 ** -20)
+        assert float((p + 0.25 * g.sign()).abs().max()) <= tol, k
+        if bits == 8:
+            assert bool((st.exp_avg_sq[0].float() == 448).all())
