@@ -23,9 +23,9 @@
 // is not 0 is never stored as 0: its weight would move by m / eps.
 //
 // 32-bit states are bound by HBM: 434 M weights, most bf16 with masters (12.1 GB), 1702 us, 7.1 TB/s,
-// above the copy rate since more is read than written.  8-bit states by instructions, 55 for
+// above the copy rate since more is read than written.  8-bit states by instructions, 58 for
 // each entry (the hash, the codes and their decoding half of them): the same weights without
-// masters (4.5 GB, 668 us at the copy rate) 905 us.
+// masters (4.5 GB, 668 us at the copy rate) 908 us.
 #include <type_traits>
 
 #include "specv_internal.h"

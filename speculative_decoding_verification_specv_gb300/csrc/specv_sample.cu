@@ -37,11 +37,11 @@
 //
 // Measured, with the filtered row written in brackets.  2048 rows of 128256 fp32 entries
 // (1.05 GB, 157 us at the copy rate; 313): top-k 50 192 us (368), min-p 0.05 170 (350),
-// nothing 316 to filter; bound by HBM.  Nothing 237 to 289 to sample: the second read of an
+// nothing 316 to filter; bound by HBM.  Nothing 235 to 289 to sample: the second read of an
 // eighth of the row, and of all of it where u W lies too close to a border to tell.  top-p
 // 0.95: 300 us where every row has some likely entries, 691 where all are flat: bound by
 // instructions, some forty for each entry of the pass over the whole row; one flat row of
-// bf16 66.  One with top-k 50 and top-p 0.9 17 us, bound by a dozen barriers and loads that
+// bf16 66.  One with top-k 50 and top-p 0.9 16 us, bound by a dozen barriers and loads that
 // wait for one another.
 #include "specv_internal.h"
 #include "specv_rowstat.cuh"
